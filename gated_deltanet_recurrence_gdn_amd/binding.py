@@ -6,8 +6,10 @@ the import of this module raises: there is no fallback implementation.
 
 Raw functions (``gdn_create``, ``gdn_forward``, ``gdn_forward_bidi``,
 ``gdn_forward_packed``, ``gdn_forward_bidi_packed``, ``gdn_forward_noalloc``, ``gdn_free``,
-``gdn_last_error``, ``gdn_version``) take device pointers as ints or torch tensors and return the C
-status.  ``GDN`` wraps a handle for torch callers.
+``gdn_last_error``, ``gdn_version``; around the recurrence ``gdn_rotary``, ``gdn_glr_create``,
+``gdn_glr_forward``, ``gdn_glr_backward``, ``gdn_group_norm_create``, ``gdn_group_norm_forward``,
+``gdn_group_norm_backward``) take device pointers as ints or torch tensors and return the C
+status.  ``GDN``, ``GLR`` and ``GroupNorm`` wrap a handle for torch callers, ``rotary`` a call.
 """
 from __future__ import annotations
 
@@ -32,12 +34,35 @@ GDN_BF16 = 1
 GDN_FP8 = 2
 GDN_FLAG_BIDI = 1
 GDN_FLAG_SEGMENTS = 2
+GDN_FLAG_REVERSE = 4
+GDN_ROTARY_HALVES = 1
+GDN_ROTARY_INVERSE = 2
+GDN_ACT_NONE = 0
+GDN_ACT_SILU = 1
+GDN_GLR_SAVED_TOKENS = 128
 
 
 class gdn_config(ctypes.Structure):
     _fields_ = [("device", ctypes.c_int), ("B", ctypes.c_int), ("H", ctypes.c_int),
                 ("d_k", ctypes.c_int), ("d_v", ctypes.c_int), ("io_dtype", ctypes.c_int),
                 ("max_T", ctypes.c_longlong), ("flags", ctypes.c_uint)]
+
+
+class gdn_rotary_config(ctypes.Structure):
+    _fields_ = [("device", ctypes.c_int), ("B", ctypes.c_int), ("H", ctypes.c_int), ("d", ctypes.c_int),
+                ("io_dtype", ctypes.c_int), ("axis_dim", ctypes.c_int * 3), ("theta", ctypes.c_double),
+                ("flags", ctypes.c_uint)]
+
+
+class gdn_glr_config(ctypes.Structure):
+    _fields_ = [("device", ctypes.c_int), ("B", ctypes.c_int), ("H", ctypes.c_int), ("d", ctypes.c_int),
+                ("io_dtype", ctypes.c_int), ("gate_dim", ctypes.c_int), ("max_T", ctypes.c_longlong),
+                ("flags", ctypes.c_uint)]
+
+
+class gdn_group_norm_config(ctypes.Structure):
+    _fields_ = [("device", ctypes.c_int), ("C", ctypes.c_int), ("G", ctypes.c_int), ("io_dtype", ctypes.c_int),
+                ("act", ctypes.c_int), ("eps", ctypes.c_float), ("max_N", ctypes.c_longlong)]
 
 
 class GDNError(RuntimeError):
@@ -69,6 +94,20 @@ def _load():
     lib.gdn_forward_bidi_packed.restype = I
     lib.gdn_forward_noalloc.argtypes = [ctypes.POINTER(gdn_config), P, P, P, P, P, P, P, P, LL, I, P]
     lib.gdn_forward_noalloc.restype = I
+    lib.gdn_rotary.argtypes = [ctypes.POINTER(gdn_rotary_config), P, LL, LL, P, LL, LL, P, LL, LL, I, I, LL, P]
+    lib.gdn_rotary.restype = I
+    lib.gdn_glr_create.argtypes = [ctypes.POINTER(gdn_glr_config), ctypes.POINTER(ctypes.c_void_p)]
+    lib.gdn_glr_create.restype = I
+    lib.gdn_glr_forward.argtypes = [P, P, P, P, P, P, P, P, LL, P]
+    lib.gdn_glr_forward.restype = I
+    lib.gdn_glr_backward.argtypes = [P, P, P, P, P, P, P, P, P, P, P, LL, P]
+    lib.gdn_glr_backward.restype = I
+    lib.gdn_group_norm_create.argtypes = [ctypes.POINTER(gdn_group_norm_config), ctypes.POINTER(ctypes.c_void_p)]
+    lib.gdn_group_norm_create.restype = I
+    lib.gdn_group_norm_forward.argtypes = [P, P, P, P, P, P, LL, LL, P]
+    lib.gdn_group_norm_forward.restype = I
+    lib.gdn_group_norm_backward.argtypes = [P, P, P, P, P, P, P, P, P, LL, LL, P]
+    lib.gdn_group_norm_backward.restype = I
     lib.gdn_free.argtypes = [P]
     lib.gdn_free.restype = None
     lib.gdn_last_error.argtypes = [P]
@@ -144,6 +183,51 @@ def gdn_forward_noalloc(cfg: gdn_config, q, k, v, beta, decay, state_in, state_o
     read with gdn_last_error(None)."""
     return _lib.gdn_forward_noalloc(ctypes.byref(cfg), _p(q), _p(k), _p(v), _p(beta), _p(decay), _p(state_in),
                                     _p(state_out), _p(out), int(T), int(chunk_len), stream)
+
+
+def gdn_rotary(cfg: gdn_rotary_config, x, x_token_stride: int, x_batch_stride: int, out, out_token_stride: int,
+               out_batch_stride: int, positions, positions_batch_stride: int, first_token: int, height: int,
+               width: int, T: int, stream=None) -> int:
+    """No handle: errors are read with gdn_last_error(None)."""
+    return _lib.gdn_rotary(ctypes.byref(cfg), _p(x), int(x_token_stride), int(x_batch_stride), _p(out),
+                           int(out_token_stride), int(out_batch_stride), _p(positions), int(positions_batch_stride),
+                           int(first_token), int(height), int(width), int(T), stream)
+
+
+def gdn_glr_create(device: int, B: int, H: int, d: int, io_dtype: int, gate_dim: int, max_T: int, flags: int = 0):
+    """Returns (status, handle); handle is None on failure."""
+    cfg = gdn_glr_config(device, B, H, d, io_dtype, gate_dim, max_T, flags)
+    h = ctypes.c_void_p()
+    st = _lib.gdn_glr_create(ctypes.byref(cfg), ctypes.byref(h))
+    return st, (h.value if st == GDN_OK else None)
+
+
+def gdn_glr_forward(h, v, beta, decay, state_in, state_out, saved, out, T: int, stream=None) -> int:
+    return _lib.gdn_glr_forward(h, _p(v), _p(beta), _p(decay), _p(state_in), _p(state_out), _p(saved), _p(out),
+                                int(T), stream)
+
+
+def gdn_glr_backward(h, v, beta, decay, saved, dout, dstate_out, dv, dbeta, ddecay, dstate_in, T: int,
+                     stream=None) -> int:
+    return _lib.gdn_glr_backward(h, _p(v), _p(beta), _p(decay), _p(saved), _p(dout), _p(dstate_out), _p(dv),
+                                 _p(dbeta), _p(ddecay), _p(dstate_in), int(T), stream)
+
+
+def gdn_group_norm_create(device: int, C: int, G: int, io_dtype: int, act: int, eps: float, max_N: int):
+    """Returns (status, handle); handle is None on failure."""
+    cfg = gdn_group_norm_config(device, C, G, io_dtype, act, eps, max_N)
+    h = ctypes.c_void_p()
+    st = _lib.gdn_group_norm_create(ctypes.byref(cfg), ctypes.byref(h))
+    return st, (h.value if st == GDN_OK else None)
+
+
+def gdn_group_norm_forward(h, x, weight, bias, out, stats, N: int, S: int, stream=None) -> int:
+    return _lib.gdn_group_norm_forward(h, _p(x), _p(weight), _p(bias), _p(out), _p(stats), int(N), int(S), stream)
+
+
+def gdn_group_norm_backward(h, x, weight, bias, stats, dout, dx, dweight, dbias, N: int, S: int, stream=None) -> int:
+    return _lib.gdn_group_norm_backward(h, _p(x), _p(weight), _p(bias), _p(stats), _p(dout), _p(dx), _p(dweight),
+                                        _p(dbias), int(N), int(S), stream)
 
 
 def current_stream():
@@ -292,3 +376,240 @@ class GDN:
         self._check(gdn_forward_bidi_packed(self.h, qkv, ts, bs, beta_logit, decay_logit, out, T, chunk_len,
                                             current_stream()))
         return out
+
+
+# ---- the operators around the recurrence ------------------------------------------
+
+_IO = {"bf16": GDN_BF16, "fp32": GDN_F32, "fp8": GDN_FP8}
+
+
+def _dtype_name(dtype):
+    """Name of a torch dtype that q, k, v, x may have."""
+    import torch
+    names = {torch.bfloat16: "bf16", torch.float32: "fp32", torch.float8_e4m3fn: "fp8"}
+    if dtype not in names:
+        raise ValueError(f"expected bfloat16, float32 or float8_e4m3fn, got {dtype}")
+    return names[dtype]
+
+
+def _expect(device, *tensors):
+    """Shape, dtype, layout and device of (name, tensor or None, shape, dtype): the C ABI takes
+    raw pointers and cannot know extents, so a wrong one is refused here."""
+    for name, x, shape, want in tensors:
+        if x is None:
+            continue
+        if tuple(x.shape) != tuple(shape) or x.dtype != want or not x.is_contiguous():
+            raise ValueError(f"{name}: expected contiguous {want} {tuple(shape)}, got {x.dtype} {tuple(x.shape)}")
+        if x.device.type != "cuda" or x.device.index != device:
+            raise ValueError(f"{name}: expected a tensor on cuda:{device}, got {x.device}")
+
+
+def _stream_of(device: int):
+    """The raw hipStream_t of torch's current stream on that device (not of the current device's)."""
+    import torch
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def rotary(x, axis_dims, theta=10000.0, positions=None, grid=None, first_token=0, halves=False, inverse=False,
+           out=None):
+    """Rotary positions over (time, height, width) for x [B, T, H, d] (any strides with the heads of a
+    token side by side; q and k of a packed projection are one x of twice the heads).
+
+    axis_dims: elements of a head turned by each axis; positions: int32 [B, T, 3] or [T, 3] (the same for
+    every batch element), or None for a raster grid=(height, width) whose first token is first_token.
+    halves: pairs (i, i + dim/2) instead of (2i, 2i+1).  inverse: the negative angles, which is the
+    gradient with respect to x.  out may be x (in place).  Returns out (fp32 for fp32 x, else bf16).
+    """
+    import torch
+    io = _IO[_dtype_name(x.dtype)]
+    odt = torch.float32 if io == GDN_F32 else torch.bfloat16
+    if x.dim() != 4 or x.device.type != "cuda":
+        raise ValueError(f"x: expected a [B, T, H, d] tensor on a GPU, got {tuple(x.shape)} on {x.device}")
+    B, T, H, d = x.shape
+    if out is None:
+        out = torch.empty((B, T, H, d), dtype=odt, device=x.device)
+    elif tuple(out.shape) != (B, T, H, d) or out.dtype != odt or out.device != x.device:
+        raise ValueError(f"out: expected {odt} {(B, T, H, d)} on {x.device}, got {out.dtype} {tuple(out.shape)}")
+    if 0 in (B, H, d) or T == 0:
+        return out
+    for name, y in (("x", x), ("out", out)):
+        if (d > 1 and y.stride(3) != 1) or (H > 1 and y.stride(2) != d):
+            raise ValueError(f"{name}: the heads of a token must lie side by side, got strides {y.stride()}")
+    pbs = 0
+    if positions is not None:
+        if positions.dtype != torch.int32 or positions.device != x.device or not positions.is_contiguous() or \
+                tuple(positions.shape) not in ((T, 3), (B, T, 3)):
+            raise ValueError(f"positions: expected contiguous int32 {(T, 3)} or {(B, T, 3)} on {x.device}, "
+                             f"got {positions.dtype} {tuple(positions.shape)} on {positions.device}")
+        pbs = 3 * T if positions.dim() == 3 else 0
+        height = width = 1
+        first_token = 0
+    elif grid is None:
+        raise ValueError("positions or grid must be given")
+    else:
+        height, width = grid
+    dt, dy, dx = axis_dims
+    flags = (GDN_ROTARY_HALVES if halves else 0) | (GDN_ROTARY_INVERSE if inverse else 0)
+    cfg = gdn_rotary_config(x.device.index, B, H, d, io, (ctypes.c_int * 3)(dt, dy, dx), theta, flags)
+    # a dimension of one has no stride of its own
+    xts, ots = (y.stride(1) if T > 1 else H * d for y in (x, out))
+    xbs, obs = (y.stride(0) if B > 1 else 0 for y in (x, out))
+    st = gdn_rotary(cfg, x, xts, xbs, out, ots, obs, positions, pbs, first_token, height, width, T,
+                    _stream_of(x.device.index))
+    if st != GDN_OK:
+        raise GDNError(st, gdn_last_error(None))
+    return out
+
+
+class _Handle:
+    """A handle of the library: freed on close, as a context manager and with the object."""
+
+    h = None
+
+    def _open(self, made):
+        self._free = _lib.gdn_free  # kept on the object: usable while the interpreter shuts down
+        st, h = made
+        if st != GDN_OK:
+            raise GDNError(st, gdn_last_error(None))
+        self.h = h
+
+    def close(self):
+        if self.h is not None:
+            self._free(self.h)
+            self.h = None
+
+    __del__ = close
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+    def _check(self, st):
+        if st != GDN_OK:
+            raise GDNError(st, gdn_last_error(self.h))
+
+    def _torch_types(self, dtype):
+        """(dtype of the input, dtype of the outputs): outputs are fp32 for fp32 inputs, bf16 otherwise."""
+        import torch
+        return {"bf16": (torch.bfloat16, torch.bfloat16), "fp32": (torch.float32, torch.float32),
+                "fp8": (torch.float8_e4m3fn, torch.bfloat16)}[dtype]
+
+
+class GLR(_Handle):
+    """The diagonal gated linear recurrence h_t = a_t h_{t-1} + b_t v_t, for torch callers: a handle bound
+    to one (device, B, H, d, dtype, gate, max_T).  gate "head": beta and decay [B, T, H]; "channel":
+    [B, T, H, d].  reverse walks the tokens from the last to the first."""
+
+    def __init__(self, B, H, d, dtype="bf16", max_T=0, device=0, gate="head", reverse=False):
+        self.B, self.H, self.d, self.dtype, self.device = B, H, d, dtype, device
+        self.gate_dim = {"head": 1, "channel": d}[gate]
+        self._open(gdn_glr_create(device, B, H, d, _IO[dtype], self.gate_dim, max_T,
+                                  GDN_FLAG_REVERSE if reverse else 0))
+
+    def _shapes(self, T):
+        B, H, d = self.B, self.H, self.d
+        tok = (B, T, H, d)
+        return tok, ((B, T, H) if self.gate_dim == 1 else tok), (B, H, d), (B, -(-T // GDN_GLR_SAVED_TOKENS), H, d)
+
+    def _inputs(self, v, beta, decay):
+        import torch
+        if v.dim() != 4:
+            raise ValueError(f"v: expected [B, T, H, d], got {tuple(v.shape)}")
+        T = v.shape[1]
+        tok, gate, _, _ = self._shapes(T)
+        dt, _ = self._torch_types(self.dtype)
+        _expect(self.device, ("v", v, tok, dt), ("beta", beta, gate, torch.float32),
+                ("decay", decay, gate, torch.float32))
+        return T
+
+    def _forward(self, v, beta, decay, state_in, state_out, out, return_state, saved):
+        import torch
+        T = self._inputs(v, beta, decay)
+        tok, _, st, sv = self._shapes(T)
+        _, odt = self._torch_types(self.dtype)
+        f32 = torch.float32
+        _expect(self.device, ("state_in", state_in, st, f32), ("state_out", state_out, st, f32), ("out", out, tok, odt))
+        if out is None:
+            out = torch.empty(tok, dtype=odt, device=v.device)
+        if state_out is None and return_state:
+            state_out = torch.empty(st, dtype=f32, device=v.device)
+        saved = torch.empty(sv, dtype=f32, device=v.device) if saved else None
+        self._check(gdn_glr_forward(self.h, v, beta, decay, state_in, state_out, saved, out, T,
+                                    _stream_of(self.device)))
+        return out, state_out, saved
+
+    def forward(self, v, beta, decay, state_in=None, state_out=None, out=None, return_state=True):
+        """Returns (out, state_out).  beta None = 1.  state_out may be state_in (in place)."""
+        return self._forward(v, beta, decay, state_in, state_out, out, return_state, False)[:2]
+
+    def forward_train(self, v, beta, decay, state_in=None, state_out=None, out=None, return_state=True):
+        """Returns (out, state_out, saved); saved goes to ``backward``."""
+        return self._forward(v, beta, decay, state_in, state_out, out, return_state, True)
+
+    def backward(self, v, beta, decay, saved, dout, dstate_out=None):
+        """The gradient of ``forward_train`` at the same v, beta, decay and its saved.  Returns
+        (dv, dbeta, ddecay, dstate_in); dbeta is None without beta."""
+        import torch
+        T = self._inputs(v, beta, decay)
+        tok, gate, st, sv = self._shapes(T)
+        _, odt = self._torch_types(self.dtype)
+        f32 = torch.float32
+        _expect(self.device, ("saved", saved, sv, f32), ("dout", dout, tok, odt), ("dstate_out", dstate_out, st, f32))
+        dv = torch.empty(tok, dtype=odt, device=v.device)
+        dbeta = None if beta is None else torch.empty(gate, dtype=f32, device=v.device)
+        ddecay = torch.empty(gate, dtype=f32, device=v.device)
+        dstate_in = torch.empty(st, dtype=f32, device=v.device)
+        self._check(gdn_glr_backward(self.h, v, beta, decay, saved, dout, dstate_out, dv, dbeta, ddecay, dstate_in, T,
+                                     _stream_of(self.device)))
+        return dv, dbeta, ddecay, dstate_in
+
+
+class GroupNorm(_Handle):
+    """Group norm with an activation ("silu" or "none"), channels last, for torch callers: a handle bound
+    to one (device, C, G, dtype, act, eps) and samples up to max_N.  x is [N, ..., C]: every dimension
+    between is part of the sample; [N, C] normalises each row (N = B T tokens, a group per head)."""
+
+    def __init__(self, C, G, dtype="bf16", act="silu", eps=1e-5, max_N=1, device=0):
+        self.C, self.G, self.dtype, self.device = C, G, dtype, device
+        self._open(gdn_group_norm_create(device, C, G, _IO[dtype], {"none": GDN_ACT_NONE, "silu": GDN_ACT_SILU}[act],
+                                         eps, max_N))
+
+    def _inputs(self, x, weight, bias):
+        import torch
+        dt, _ = self._torch_types(self.dtype)
+        if x.dim() < 2:
+            raise ValueError(f"x: expected [N, ..., C], got {tuple(x.shape)}")
+        N, S = x.shape[0], 1
+        for n in x.shape[1:-1]:
+            S *= n
+        _expect(self.device, ("x", x, (*x.shape[:-1], self.C), dt), ("weight", weight, (self.C,), torch.float32),
+                ("bias", bias, (self.C,), torch.float32))
+        return N, S
+
+    def forward(self, x, weight=None, bias=None, out=None, return_stats=True):
+        """Returns (out, stats); stats [N, G, 2] (mean, 1 / sqrt(var + eps)) goes to ``backward``."""
+        import torch
+        N, S = self._inputs(x, weight, bias)
+        _, odt = self._torch_types(self.dtype)
+        _expect(self.device, ("out", out, x.shape, odt))
+        if out is None:
+            out = torch.empty(x.shape, dtype=odt, device=x.device)
+        stats = torch.empty((N, self.G, 2), dtype=torch.float32, device=x.device) if return_stats else None
+        self._check(gdn_group_norm_forward(self.h, x, weight, bias, out, stats, N, S, _stream_of(self.device)))
+        return out, stats
+
+    def backward(self, x, weight, bias, stats, dout):
+        """The gradient of ``forward`` at the same x, weight, bias and its stats.  Returns (dx, dweight,
+        dbias); dweight and dbias are None without weight and bias."""
+        import torch
+        N, S = self._inputs(x, weight, bias)
+        _, odt = self._torch_types(self.dtype)
+        _expect(self.device, ("stats", stats, (N, self.G, 2), torch.float32), ("dout", dout, x.shape, odt))
+        dx = torch.empty(x.shape, dtype=odt, device=x.device)
+        dweight = None if weight is None else torch.empty_like(weight)
+        dbias = None if bias is None else torch.empty_like(bias)
+        self._check(gdn_group_norm_backward(self.h, x, weight, bias, stats, dout, dx, dweight, dbias, N, S,
+                                            _stream_of(self.device)))
+        return dx, dweight, dbias

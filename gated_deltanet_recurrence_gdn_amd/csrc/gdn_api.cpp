@@ -8,6 +8,7 @@
 // never a silent fallback (the sglang SANA-WM record raises when a forced GDN
 // backend fails its prechecks).
 #include "gdn.h"
+#include "gdn_ctx.h"
 #include "gdn_launch.h"
 
 #include <hip/hip_runtime.h>
@@ -19,27 +20,8 @@
 #include <vector>
 #include <new>
 
-// Messages live in fixed buffers, so no call but gdn_create allocates host memory.
-constexpr size_t ERR_LEN = 512;
-
-struct gdn_ctx {
-    gdn_config cfg{};
-    char err[ERR_LEN] = {0};
-    float *scratch = nullptr;  // bidirectional form: two fp32 [B, max_T, H, d_v] partials, then
-                               // two fp32 [B, H, d_v, d_k] states (the MFMA kernel's split sweep)
-    size_t scratch_bytes = 0;
-    uint16_t *tm = nullptr;    // per-chunk triangular inverses of the MFMA chunked kernel
-    long long tm_chunks = 0;   // their capacity: directions x B x H x ceil(max_T / 64)
-    // bidirectional MFMA path: a second stream (default priority) and three events, so that
-    // most inverses are formed beside the first sweep launches
-    hipStream_t side = nullptr;
-    hipEvent_t ev_fork = nullptr, ev_join = nullptr, ev_join_mid = nullptr;
-    // segment-parallel causal form (GDN_FLAG_SEGMENTS on a handle the MFMA kernel serves):
-    // one allocation holding the buffers gdn::PassArgs describes, and the CU count that
-    // bounds the segment count
-    float *seg = nullptr;
-    int ncu = 0;
-};
+// Last failure of a create call, or of a call that takes no handle, on this thread.
+thread_local char g_create_err[ERR_LEN];
 
 namespace {
 // At most this many segments per call, each of at least SEG_MIN_CHUNKS 64-token chunks.
@@ -73,22 +55,6 @@ static_assert((int)GDN_F32 == (int)gdn::IO_F32 && (int)GDN_BF16 == (int)gdn::IO_
 
 namespace {
 
-// Last failure of gdn_create, or of a call that takes no handle, on this thread.
-thread_local char g_create_err[ERR_LEN];
-
-int set_err(char *dst, int code, const char *fmt, va_list ap) {
-    vsnprintf(dst, ERR_LEN, fmt, ap);
-    return code;
-}
-
-int fail(gdn_ctx *h, int code, const char *fmt, ...) {
-    va_list ap;
-    va_start(ap, fmt);
-    set_err(h->err, code, fmt, ap);
-    va_end(ap);
-    return code;
-}
-
 int fail_create(int code, const char *fmt, ...) {
     va_list ap;
     va_start(ap, fmt);
@@ -99,51 +65,6 @@ int fail_create(int code, const char *fmt, ...) {
 }
 
 bool valid_dim(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
-
-struct Range {
-    const char *name;
-    uintptr_t lo, hi;  // [lo, hi)
-};
-
-bool overlap(const Range &a, const Range &b) {
-    return a.hi > a.lo && b.hi > b.lo && a.lo < b.hi && b.lo < a.hi;
-}
-
-Range rng(const char *name, const void *p, size_t bytes) {
-    uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return Range{name, lo, p ? lo + bytes : lo};
-}
-
-// Checks that p is device memory of `device` (not host memory, which would
-// fault on the GPU).  Skipped for dry-run handles.
-int check_device_ptr(gdn_ctx *h, const char *name, const void *p) {
-    if (!p || h->cfg.device < 0) return GDN_OK;
-    hipPointerAttribute_t attr;
-    hipError_t e = hipPointerGetAttributes(&attr, p);
-    if (e != hipSuccess) {
-        (void)hipGetLastError();
-        return fail(h, GDN_ERR_ARG, "%s: not a HIP allocation (%s)", name, hipGetErrorString(e));
-    }
-    if (attr.type != hipMemoryTypeDevice && attr.type != hipMemoryTypeManaged)
-        return fail(h, GDN_ERR_ARG, "%s: not device memory", name);
-    if (attr.device != h->cfg.device)
-        return fail(h, GDN_ERR_ARG, "%s: lives on device %d, handle is on device %d", name,
-                    attr.device, h->cfg.device);
-    return GDN_OK;
-}
-
-struct DeviceGuard {
-    int prev = -1;
-    bool changed = false;
-    explicit DeviceGuard(int dev) {
-        if (hipGetDevice(&prev) == hipSuccess && prev != dev) {
-            changed = hipSetDevice(dev) == hipSuccess;
-        }
-    }
-    ~DeviceGuard() {
-        if (changed) (void)hipSetDevice(prev);
-    }
-};
 
 // Largest token stride (elements) of q, k, v: the kernels address up to 64
 // tokens of a chunk with 32-bit offsets from the chunk's first token.
@@ -285,15 +206,6 @@ int check_aliasing(gdn_ctx *h, const Range *outs, int n_out, const Range *ins, i
     return GDN_OK;
 }
 
-int launch_status(gdn_ctx *h, hipError_t e, const char *what) {
-    if (e == hipSuccess) e = hipGetLastError();
-    if (e != hipSuccess) {
-        (void)hipGetLastError();
-        return fail(h, GDN_ERR_LAUNCH, "%s launch failed: %s", what, hipGetErrorString(e));
-    }
-    return GDN_OK;
-}
-
 int resolve_chunk(gdn_ctx *h, int chunk_len, int *C) {
     if (chunk_len == 0) chunk_len = 64;
     if (chunk_len == 1) {
@@ -343,7 +255,7 @@ int check_config(const gdn_config &c, unsigned allowed, char *err) {
 
 extern "C" {
 
-const char *gdn_version(void) { return "0.2.0"; }
+const char *gdn_version(void) { return "0.3.0"; }
 
 int gdn_create(const gdn_config *cfg, gdn_handle *out_h) {
     if (out_h) *out_h = nullptr;
@@ -458,6 +370,7 @@ int gdn_create(const gdn_config *cfg, gdn_handle *out_h) {
         return fail_create(GDN_ERR_OOM, "out of host memory");
     }
     h->cfg = c;
+    h->device = c.device;
     h->scratch = scratch;
     h->scratch_bytes = scratch_bytes;
     h->tm = tm;
@@ -475,8 +388,9 @@ int gdn_create(const gdn_config *cfg, gdn_handle *out_h) {
 
 void gdn_free(gdn_handle h) {
     if (!h) return;
-    if (h->scratch || h->tm || h->side || h->seg) {
-        DeviceGuard g(h->cfg.device);
+    if (h->scratch || h->tm || h->side || h->seg || h->work) {
+        DeviceGuard g(h->device);
+        if (h->work) (void)hipFree(h->work);
         if (h->seg) (void)hipFree(h->seg);
         if (h->ev_join_mid) (void)hipEventDestroy(h->ev_join_mid);
         if (h->ev_join) (void)hipEventDestroy(h->ev_join);
@@ -641,6 +555,7 @@ int gdn_forward(gdn_handle h, const void *q, const void *k, const void *v, const
         return GDN_ERR_ARG;
     }
     h->err[0] = 0;
+    if (int kind = check_kind(h, KIND_GDN, "gdn_forward")) return kind;
     Inputs in;
     size_t out_bytes;
     int st = prepare_plain(h, q, k, v, beta, decay, out, T, &in, &out_bytes);
@@ -656,6 +571,7 @@ int gdn_forward_packed(gdn_handle h, const void *qkv, long long token_stride, lo
         return GDN_ERR_ARG;
     }
     h->err[0] = 0;
+    if (int kind = check_kind(h, KIND_GDN, "gdn_forward_packed")) return kind;
     Inputs in;
     size_t out_bytes;
     int st = prepare_packed(h, qkv, token_stride, batch_stride, beta_logit, decay_logit, out, T, &in, &out_bytes);
@@ -670,6 +586,7 @@ int gdn_forward_bidi(gdn_handle h, const void *q, const void *k, const void *v, 
         return GDN_ERR_ARG;
     }
     h->err[0] = 0;
+    if (int kind = check_kind(h, KIND_GDN, "gdn_forward_bidi")) return kind;
     int st = need_bidi(h, "gdn_forward_bidi");
     if (st) return st;
     Inputs in;
@@ -686,6 +603,7 @@ int gdn_forward_bidi_packed(gdn_handle h, const void *qkv, long long token_strid
         return GDN_ERR_ARG;
     }
     h->err[0] = 0;
+    if (int kind = check_kind(h, KIND_GDN, "gdn_forward_bidi_packed")) return kind;
     int st = need_bidi(h, "gdn_forward_bidi_packed");
     if (st) return st;
     Inputs in;
@@ -709,6 +627,7 @@ int gdn_forward_noalloc(const gdn_config *cfg, const void *q, const void *k, con
     }
     gdn_ctx ctx;
     ctx.cfg = *cfg;
+    ctx.device = cfg->device;
     ctx.cfg.max_T = T < 0 ? 0 : T;  // the limit is the fixed scratch, checked below
     g_create_err[0] = 0;
     int st = check_config(ctx.cfg, 0u, g_create_err);

@@ -236,11 +236,179 @@ int gdn_forward_noalloc(const gdn_config *cfg, const void *q, const void *k,
                         const float *state_in, float *state_out, void *out,
                         long long T, int chunk_len, void *hip_stream);
 
+/* ======================================================================== *
+ * Operators around the recurrence: rotary positions for q and k, the        *
+ * diagonal gated linear recurrence with its gradient, and group norm with   *
+ * an activation, channels last, with its gradient.  Device pointers, types, *
+ * streams, ownership, status codes and messages as above: nothing is        *
+ * allocated, synchronised or copied by a call, every argument is checked    *
+ * before the first launch, and a call can be captured into a HIP graph.     *
+ * Outputs are fp32 for GDN_F32 and bf16 for GDN_BF16 and GDN_FP8.  Results  *
+ * are the same bits on every run of a call.                                 *
+ * ======================================================================== */
+
+/*
+ * Rotary positions over three axes (time, height, width).  Head dim d is cut
+ * into sections of axis_dim[0], axis_dim[1] and axis_dim[2] elements, in that
+ * order; what is left of d passes through.  In section s the pair (x, y) number
+ * i = 0 .. axis_dim[s] / 2 - 1 is turned by the angle
+ *     p_s * theta^(-2 i / axis_dim[s]),    p_s the token's position on axis s:
+ *     (x, y) -> (x cos - y sin, x sin + y cos),
+ * where pair i is elements (2i, 2i + 1) of the section, or (i, i +
+ * axis_dim[s] / 2) with GDN_ROTARY_HALVES.  GDN_ROTARY_INVERSE turns by the
+ * negative angles: the inverse, and the gradient with respect to x.  Angles are
+ * formed and reduced in 64 bits (positions far from 0 lose nothing); the turn
+ * is fp32, rounded once.
+ *
+ * The turn keeps a pair's length, so q and k may be turned before the L2
+ * normalisation of gdn_forward_packed: turn the first 2 H heads of the packed
+ * rows (H here = 2 * heads) in place, then call it.
+ */
+#define GDN_ROTARY_HALVES 1u
+#define GDN_ROTARY_INVERSE 2u
+
+typedef struct {
+    int device;       /* HIP device ordinal; -1 = dry run (validate only, no GPU)    */
+    int B, H;         /* batch and heads per token row, each >= 1                    */
+    int d;            /* head dim, a multiple of 8, 8 .. 512                         */
+    int io_dtype;     /* gdn_dtype of x                                              */
+    int axis_dim[3];  /* elements turned by time, height, width: even, >= 0, sum <= d */
+    double theta;     /* base of the frequencies, > 0 and finite                     */
+    unsigned flags;   /* GDN_ROTARY_* bits                                           */
+} gdn_rotary_config;
+
+/*
+ * Element e of head h of token t of batch element b is
+ * x[b * x_batch_stride + t * x_token_stride + h * d + e], out likewise with its
+ * own strides: token strides >= H * d and <= 2^24, batch strides >= 0, all in
+ * elements and multiples of 16 bytes (FP8: 8); x and out 16-byte (FP8: 8) aligned.  With B > 1 the
+ * batch elements of out must not overlap (out_batch_stride >= (T - 1) *
+ * out_token_stride + H * d).  out may be x itself with the same strides (in place;
+ * not for GDN_FP8); any other overlap of their byte ranges is refused.
+ *   positions  int32, the (time, height, width) position of token t of batch
+ *              element b at positions[b * positions_batch_stride + 3 t + 0 .. 2];
+ *              positions_batch_stride 0 = the same for every batch element.
+ *              NULL = a raster grid: token t has n = first_token + t and the
+ *              position (n / (height * width), n / width % height, n % width).
+ *   first_token, height, width   the raster grid (first_token >= 0, height and
+ *              width >= 1, first_token + T <= 2^31 * height * width; not read
+ *              with positions).
+ * Takes no handle: the message of a failed call is gdn_last_error(NULL).  The
+ * first call on a device checks it (hipGetDeviceProperties): make it outside
+ * graph capture.  T = 0 is valid and writes nothing.
+ */
+int gdn_rotary(const gdn_rotary_config *cfg, const void *x, long long x_token_stride,
+               long long x_batch_stride, void *out, long long out_token_stride,
+               long long out_batch_stride, const int *positions,
+               long long positions_batch_stride, long long first_token, int height,
+               int width, long long T, void *hip_stream);
+
+/*
+ * Diagonal gated linear recurrence, per batch element, head and channel:
+ *     h_t = a_t * h_{t-1} + b_t * v_t,      out_t = h_t,
+ * the recurrence above with a vector state and no keys.  a (decay) and b (beta)
+ * are plain values in [0, 1], one per token and head, or one per token, head and
+ * channel; beta may be NULL (b = 1).  a_t = 0 starts anew at token t, so
+ * sequences laid end to end need no other mark.  With GDN_FLAG_REVERSE the
+ * tokens are walked from T-1 to 0: state_in is then the state behind the last
+ * token, state_out that of token 0.
+ *     v, out, dout, dv    [B, T, H, d]        io_dtype / output type
+ *     beta, decay, dbeta, ddecay
+ *                         [B, T, H]           float32 (gate_dim = 1)
+ *                         [B, T, H, d]        float32 (gate_dim = d)
+ *     states, dstates     [B, H, d]           float32
+ *     saved               [B, ceil(T / GDN_GLR_SAVED_TOKENS), H, d] float32: the
+ *                         state before every such tile of tokens, in walking order
+ * All contiguous and 16-byte aligned, but gates of gate_dim 1 to 4 bytes.
+ */
+#define GDN_FLAG_REVERSE 4u
+#define GDN_GLR_SAVED_TOKENS 128
+
+typedef struct {
+    int device;       /* HIP device ordinal; -1 = dry run                            */
+    int B, H;         /* batch 1 .. 32767, heads >= 1, H * d <= 2^20                  */
+    int d;            /* channels of a head: 16, 32, 64 or 128                       */
+    int io_dtype;     /* gdn_dtype of v                                              */
+    int gate_dim;     /* 1 or d: gates per token and head, or per channel            */
+    long long max_T;  /* largest T any call on this handle will pass, >= 0           */
+    unsigned flags;   /* GDN_FLAG_REVERSE or 0                                       */
+} gdn_glr_config;
+
+/* As gdn_create; free with gdn_free, messages from gdn_last_error.  The handle
+ * owns a workspace that its calls share (see Ownership above). */
+int gdn_glr_create(const gdn_glr_config *cfg, gdn_handle *out_h);
+
+/*
+ * state_in NULL = zeros; state_out NULL = discarded, may equal state_in; saved
+ * NULL = not wanted (needed by gdn_glr_backward).  T = 0: state_out receives
+ * state_in or zeros.  No NaN or infinity is looked for: they propagate.
+ */
+int gdn_glr_forward(gdn_handle h, const void *v, const float *beta, const float *decay,
+                    const float *state_in, float *state_out, float *saved, void *out,
+                    long long T, void *hip_stream);
+
+/*
+ * The gradient of gdn_glr_forward at the same v, beta, decay and the saved of
+ * that call.  With dout and dstate_out (NULL = zeros) the gradients of out and
+ * state_out, and G_t = dout_t + a_{t+1} G_{t+1} (dstate_out added at the last
+ * token): dv = b G, dbeta = G v, ddecay_t = G_t h_{t-1}, dstate_in = a G of the
+ * first token; gates of gate_dim 1 sum over d.  dv, dbeta, ddecay and dstate_in
+ * may each be NULL (not wanted); dbeta must be NULL if beta is.  dstate_in may
+ * equal dstate_out.
+ */
+int gdn_glr_backward(gdn_handle h, const void *v, const float *beta, const float *decay,
+                     const float *saved, const void *dout, const float *dstate_out,
+                     void *dv, float *dbeta, float *ddecay, float *dstate_in,
+                     long long T, void *hip_stream);
+
+/*
+ * Group norm with an activation, channels last: x [N, S, C], the C channels in G
+ * groups of neighbours, mean and (biased) variance over the S * C / G values of
+ * each sample and group,
+ *     y = act((x - mean) / sqrt(var + eps) * weight + bias),
+ * act(z) = z or z * sigmoid(z).  With N = B * T, S = 1, C = H * d and G = H it
+ * normalises each head of the recurrence's outputs; with S the positions of a
+ * frame or clip it is the convolutional layers' form.
+ *     x, out, dout, dx    [N, S, C]  io_dtype / output type
+ *     weight, bias, dweight, dbias   [C] float32 (weight NULL = 1, bias NULL = 0)
+ *     stats               [N, G, 2]  float32: mean, 1 / sqrt(var + eps)
+ * All contiguous and 16-byte aligned.
+ */
+typedef enum { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1 } gdn_act;
+
+typedef struct {
+    int device;       /* HIP device ordinal; -1 = dry run                            */
+    int C, G;         /* channels, a multiple of 8 up to 8192, and groups; G divides C */
+    int io_dtype;     /* gdn_dtype of x                                              */
+    int act;          /* gdn_act                                                     */
+    float eps;        /* > 0 and finite                                              */
+    long long max_N;  /* largest N any call on this handle will pass, 0 .. 2^24      */
+} gdn_group_norm_config;
+
+/* As gdn_create; free with gdn_free, messages from gdn_last_error.  The handle
+ * owns a workspace that its calls share (see Ownership above). */
+int gdn_group_norm_create(const gdn_group_norm_config *cfg, gdn_handle *out_h);
+
+/* stats NULL = not wanted (needed by gdn_group_norm_backward).  N = 0 or S = 0
+ * writes nothing. */
+int gdn_group_norm_forward(gdn_handle h, const void *x, const float *weight,
+                           const float *bias, void *out, float *stats, long long N,
+                           long long S, void *hip_stream);
+
+/* The gradient of gdn_group_norm_forward at the same x, weight, bias and the
+ * stats of that call; dweight and dbias are sums over N and S.  dx, dweight and
+ * dbias may each be NULL (not wanted).  N = 0 or S = 0 sets dweight and dbias to
+ * zero. */
+int gdn_group_norm_backward(gdn_handle h, const void *x, const float *weight,
+                            const float *bias, const float *stats, const void *dout,
+                            void *dx, float *dweight, float *dbias, long long N,
+                            long long S, void *hip_stream);
+
 /* Release the handle and its scratch.  NULL is a no-op. */
 void gdn_free(gdn_handle h);
 
-/* Message of the last failed call on h (NULL: last gdn_create failure on
- * this thread).  Never NULL; "" when there was none.  Valid until the next
+/* Message of the last failed call on h (NULL: last failure of a create call, or
+ * of a call that takes no handle, on this thread).  Never NULL; "" when there was none.  Valid until the next
  * call on the same handle. */
 const char *gdn_last_error(gdn_handle h);
 
