@@ -39,7 +39,7 @@ GDN_ROTARY_HALVES = 1
 GDN_ROTARY_INVERSE = 2
 GDN_ACT_NONE = 0
 GDN_ACT_SILU = 1
-GDN_GLR_SAVED_TOKENS = 128
+GDN_GLR_SAVED_TOKENS = 64
 
 
 class gdn_config(ctypes.Structure):

@@ -28,7 +28,7 @@ struct RotaryArgs {
 };
 hipError_t launch_rotary(const RotaryArgs &a, hipStream_t stream);
 
-constexpr int GLR_TILE = 128;  // tokens between saved states
+constexpr int GLR_TILE = 64;   // tokens between saved states
 
 // One call of the diagonal recurrence or of its gradient.
 struct GlrArgs {

@@ -98,7 +98,12 @@ int make_handle(int kind, int device, size_t bytes, gdn_ctx **out) {
         if (int st = check_device(device, &ncu)) return st;
         if (bytes) {
             DeviceGuard g(device);
-            const hipError_t e = hipMalloc(&work, bytes);
+            hipError_t e = hipMalloc(&work, bytes);
+            if (e == hipSuccess) {  // workspaces start zeroed
+                e = hipMemset(work, 0, bytes);
+                if (e == hipSuccess) e = hipStreamSynchronize(nullptr);
+                if (e != hipSuccess) (void)hipFree(work);
+            }
             if (e != hipSuccess) {
                 (void)hipGetLastError();
                 return bad(GDN_ERR_OOM, "hipMalloc(%zu bytes) for the workspace: %s", bytes, hipGetErrorString(e));
@@ -307,9 +312,9 @@ int gdn_glr_create(const gdn_glr_config *cfg, gdn_handle *out_h) {
         st = bad(GDN_ERR_ARG, "gate_dim = %d must be 1 or d = %d", c.gate_dim, c.d);
     else if (c.max_T < 0) st = bad(GDN_ERR_ARG, "max_T = %lld is negative", c.max_T);
     else if (c.flags & ~GDN_FLAG_REVERSE) st = bad(GDN_ERR_ARG, "unknown flags 0x%x", c.flags);
-    else if ((double)c.B * (double)c.H * c.d * (double)c.max_T * 4.0 > 9.0e18 ||
-             (double)((c.max_T + gdn::GLR_TILE - 1) / gdn::GLR_TILE) * c.B * (double)(c.H * c.d / 16) > 2.0e9)
-        st = bad(GDN_ERR_ARG, "B * max_T * H * d is too large");
+    else if ((double)c.B * ((c.H * c.d + 127) / 128) * ((double)c.max_T / gdn::GLR_TILE + 1.0) > 4194304.0)
+        // a launch has a block of up to 512 threads for each, below 2^32 threads in all
+        st = bad(GDN_ERR_UNSUPPORTED, "B * ceil(H d / 128) * ceil(max_T / %d) exceeds 2^22", gdn::GLR_TILE);
     if (st) return refused(fn, st);
     gdn_ctx *h = nullptr;
     if ((st = make_handle(KIND_GLR, c.device, gdn::glr_work_bytes(c.B, c.H, c.d, c.max_T), &h))) return refused(fn, st);

@@ -322,11 +322,12 @@ int gdn_rotary(const gdn_rotary_config *cfg, const void *x, long long x_token_st
  * All contiguous and 16-byte aligned, but gates of gate_dim 1 to 4 bytes.
  */
 #define GDN_FLAG_REVERSE 4u
-#define GDN_GLR_SAVED_TOKENS 128
+#define GDN_GLR_SAVED_TOKENS 64
 
 typedef struct {
     int device;       /* HIP device ordinal; -1 = dry run                            */
-    int B, H;         /* batch 1 .. 32767, heads >= 1, H * d <= 2^20                  */
+    int B, H;         /* batch 1 .. 32767, heads >= 1, H * d <= 2^20, and B *
+                       * ceil(H d / 128) * ceil(max_T / 64) at most 2^22              */
     int d;            /* channels of a head: 16, 32, 64 or 128                       */
     int io_dtype;     /* gdn_dtype of v                                              */
     int gate_dim;     /* 1 or d: gates per token and head, or per channel            */

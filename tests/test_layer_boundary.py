@@ -60,7 +60,7 @@ def glr(B=2, H=3, d=64, io=gb.GDN_BF16, gate=1, max_T=1000, flags=0, device=-1):
 @pytest.mark.parametrize("over,code", [
     (dict(B=0), ARG), (dict(H=0), ARG), (dict(B=32768), UNSUP), (dict(d=48), UNSUP), (dict(H=1 << 15), UNSUP),
     (dict(io=7), UNSUP), (dict(gate=2), ARG), (dict(gate=0), ARG), (dict(max_T=-1), ARG), (dict(flags=1), ARG),
-    (dict(flags=8), ARG), (dict(max_T=1 << 60), ARG), (dict(device=-3), ARG),
+    (dict(flags=8), ARG), (dict(max_T=1 << 60), UNSUP), (dict(max_T=64 << 21), UNSUP), (dict(device=-3), ARG),
 ])
 def test_glr_create_refuses(over, code, capfd):
     st, h = glr(**over)
