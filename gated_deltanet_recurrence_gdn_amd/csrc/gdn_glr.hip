@@ -31,8 +31,12 @@ namespace {
 
 constexpr int LANES = 64, SLAB = 2 * LANES;  // channels of a block
 constexpr int WAVES = 8;
-constexpr int FWD_R = 16, BWD_R = 8;         // tokens of a wave
 constexpr int LOOK = 16;                     // how far back a tile looks at once
+
+// Tokens of a wave.  The chain costs a tile some microseconds whatever its size, so tiles are
+// as long as their inputs fit in registers with two blocks on a CU (128 registers a lane).
+constexpr int fwd_tokens(int io, bool ch) { return ch ? 16 : io == IO_F32 ? 32 : 64; }
+constexpr int bwd_tokens(int io, bool ch) { return ch ? 8 : 16; }
 
 typedef unsigned long long u64;
 
@@ -57,104 +61,140 @@ __device__ __forceinline__ bool known(u64 w, uint32_t call) {  // in every lane 
     return __all((uint32_t)(w >> 32) == call);
 }
 
-// State before tile k > 0 of this lane's channel (word `at` of tile k); one whole wave.
-// (A, H) is the tile's own map, published if the state is not there yet.
-__device__ float state_before(const Chain &c, uint32_t call, int k, size_t at, float A, float H) {
+// The maps a lane has found behind it, a channel per thread: kept in LDS, since the waves that
+// look back hold their tokens in registers meanwhile.
+struct Window {
+    float m[LOOK][SLAB], d[LOOK][SLAB];
+};
+
+// State before tile k > 0 of channel i of the slab; one whole wave.  `at` and `mat` are its
+// words of tile k in the planes end and add, and in mul (one word per head where a head has
+// one gate: `first` marks the lane that writes it).  (A, H) is the tile's own map.
+__device__ float state_before(const Chain &c, Window &win, int i, uint32_t call, int k, size_t at, size_t mat, bool first,
+                              float A, float H) {
     const size_t step = (size_t)c.slabs * SLAB;
-    bool posted = false;
+    post(c.add + at, word(call, H));
+    if (first) post(c.mul + mat, word(call, A));
     for (;;) {
-        const u64 last = peek(c.end + at - step);
-        if (known(last, call)) return value(last);
-        if (!posted) {
-            post(c.mul + at, word(call, A));
-            post(c.add + at, word(call, H));
-            posted = true;
-        }
-        // the nearest known end state within LOOK tiles, four at a time
-        int j = 0;
+        // the nearest known end state, four tiles at a time, with the maps behind it
         float s = 0.0f;
-        const int far = k < LOOK ? k : LOOK;
-        for (int j0 = 2; j0 <= far && !j; j0 += 4) {
-            u64 w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = peek(c.end + at - step * (j0 + i <= far ? j0 + i : far));
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (!j && known(w[i], call)) {
-                    j = j0 + i <= far ? j0 + i : far;
-                    s = value(w[i]);
-                }
-        }
-        bool ready = j > 0;  // a map may be missing: its tile found its state at once, and posts that
-        for (int i = j - 1; i >= 1 && ready; i -= 4) {
-            u64 m[4], d[4];
+        int j = 0;
+        bool ok = true;
+#pragma unroll 1
+        for (int g = 0; g < LOOK && g < k && !j && ok; g += 4) {
+            u64 e[4], wm[4], wd[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const size_t p = at - step * (i - q >= 1 ? i - q : 1);
-                m[q] = peek(c.mul + p);
-                d[q] = peek(c.add + p);
+                const size_t back = step * (g + q + 1 < k ? g + q + 1 : k);
+                e[q] = peek(c.end + at - back);
+                wm[q] = peek(c.mul + mat - back);
+                wd[q] = peek(c.add + at - back);
             }
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                if (i - q >= 1 && ready) {
-                    ready = known(m[q], call) && known(d[q], call);
-                    s = fmaf(value(m[q]), s, value(d[q]));
+                if (!j && ok) {
+                    if (known(e[q], call)) {
+                        j = g + q + 1;
+                        s = value(e[q]);
+                    }
+                    win.m[g + q][i] = value(wm[q]);
+                    win.d[g + q][i] = value(wd[q]);
+                    ok = g + q + 1 < k && known(wm[q], call) && known(wd[q], call);
                 }
         }
-        if (ready) return s;
+        if (j) {
+#pragma unroll 1
+            for (int q = j - 2; q >= 0; --q) s = fmaf(win.m[q][i], s, win.d[q][i]);
+            return s;
+        }
         __builtin_amdgcn_s_sleep(1);
     }
 }
 
-// Two neighbouring elements, as they lie in memory.
+// Two neighbouring elements, as they lie in memory: elements c and c + 1 of a row.
 template <int IO>
 struct Pair;
 template <>
 struct Pair<IO_F32> {
     float2 r;
-    __device__ __forceinline__ void load(const void *p, size_t i) { r = *reinterpret_cast<const float2 *>(static_cast<const float *>(p) + i); }
+    static constexpr int BYTES = 4;
+    __device__ __forceinline__ void load(const char *row, unsigned c) { r = *reinterpret_cast<const float2 *>(row + c * 4); }
+    __device__ __forceinline__ void zero() { r = make_float2(0.0f, 0.0f); }
     __device__ __forceinline__ float2 get() const { return r; }
-    static __device__ __forceinline__ void store(void *p, size_t i, float2 x) { *reinterpret_cast<float2 *>(static_cast<float *>(p) + i) = x; }
+    static __device__ __forceinline__ void store(char *row, unsigned c, float2 x) { *reinterpret_cast<float2 *>(row + c * 4) = x; }
 };
 template <>
 struct Pair<IO_BF16> {
     uint32_t r;
-    __device__ __forceinline__ void load(const void *p, size_t i) { r = *reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p) + i); }
+    static constexpr int BYTES = 2;
+    __device__ __forceinline__ void load(const char *row, unsigned c) { r = *reinterpret_cast<const uint32_t *>(row + c * 2); }
+    __device__ __forceinline__ void zero() { r = 0; }
     __device__ __forceinline__ float2 get() const { return make_float2(bf16_lo(r), bf16_hi(r)); }
-    static __device__ __forceinline__ void store(void *p, size_t i, float2 x) {
-        *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p) + i) = pack_bf16x2(x.x, x.y);
+    static __device__ __forceinline__ void store(char *row, unsigned c, float2 x) {
+        *reinterpret_cast<uint32_t *>(row + c * 2) = pack_bf16x2(x.x, x.y);
     }
 };
 template <>
 struct Pair<IO_FP8> {
-    uint16_t r;
-    __device__ __forceinline__ void load(const void *p, size_t i) { r = *reinterpret_cast<const uint16_t *>(static_cast<const uint8_t *>(p) + i); }
+    uint32_t r;
+    static constexpr int BYTES = 1;
+    __device__ __forceinline__ void load(const char *row, unsigned c) { r = *reinterpret_cast<const uint16_t *>(row + c); }
+    __device__ __forceinline__ void zero() { r = 0; }
     __device__ __forceinline__ float2 get() const {
         float f[4];
         fp8x4_to_f32(r, f);
         return make_float2(f[0], f[1]);
     }
 };
+// Makes the compiler forget what it formed from these registers: widened copies kept from one
+// pass over the tokens to the next would take twice the registers.
+template <int R, int IO>
+__device__ __forceinline__ void anew(Pair<IO> (&v)[R]) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        if constexpr (IO == IO_F32)
+            asm volatile("" : "+v"(v[r].r.x), "+v"(v[r].r.y));
+        else
+            asm volatile("" : "+v"(v[r].r));
+    }
+}
+// Keeps the loads of one stretch of tokens from being moved before those of the last.
+__device__ __forceinline__ void stretch(int r) {
+    if (r % 8 == 0) __builtin_amdgcn_sched_barrier(0);
+}
 template <int IO>
 using OutPair = Pair<IO == IO_F32 ? IO_F32 : IO_BF16>;
 
-// A gate of two channels: one value per channel, or the head's (d is even, so a lane's
-// channels are of one head).
-template <bool CH>
-struct Gate;
-template <>
-struct Gate<true> {
-    float2 r;
-    __device__ __forceinline__ void load(const float *p, size_t row, int C, int, int c, int) { r = *reinterpret_cast<const float2 *>(p + row * C + c); }
-    __device__ __forceinline__ float2 get() const { return r; }
-    __device__ __forceinline__ void set(float x) { r = make_float2(x, x); }
+// The gates of a wave's R tokens.  Per channel: in registers.  Per head: the tile's gates of
+// the slab's heads are staged in LDS by the block (one load per token and head instead of one
+// per lane) as a row of tokens per head, and read from there where they are used; a row's
+// pitch of four more keeps the up to eight heads of a wave on different banks.
+template <bool CH, int R>
+struct Gates;
+template <int R>
+struct Gates<true, R> {
+    float2 r[R];
+    static constexpr int STAGE = 1;
+    __device__ __forceinline__ float2 get(int i) const { return r[i]; }
 };
-template <>
-struct Gate<false> {
-    float r;
-    __device__ __forceinline__ void load(const float *p, size_t row, int, int H, int, int h) { r = p[row * H + h]; }
-    __device__ __forceinline__ float2 get() const { return make_float2(r, r); }
-    __device__ __forceinline__ void set(float x) { r = x; }
+template <int R>
+struct Gates<false, R> {
+    const float *r;
+    static constexpr int PITCH = WAVES * R + 4, STAGE = PITCH * (SLAB / 16);
+    // The whole block, before the barrier that precedes get.  Past the end stands `past`.
+    __device__ __forceinline__ void stage(float *lds, const float *p, const GlrArgs &a, int b, int slab_c0, long long tile0,
+                                          int tokens, float past) {
+        const int heads = SLAB / a.d, h0 = slab_c0 / a.d;
+        for (int i = threadIdx.x; i < tokens * heads; i += blockDim.x) {
+            const long long t = tile0 + i / heads;
+            const int h = h0 + i % heads < a.H ? h0 + i % heads : a.H - 1;
+            lds[i % heads * PITCH + i / heads] = t < a.T ? p[((size_t)b * a.T + (a.reverse ? a.T - 1 - t : t)) * a.H + h] : past;
+        }
+    }
+    __device__ __forceinline__ void place(const float *lds, int wave, int lane, int d) {
+        r = lds + 2 * lane / d * PITCH + wave * R;
+    }
+    __device__ __forceinline__ float2 get(int i) const { return make_float2(r[i], r[i]); }
 };
 
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y)); }
@@ -183,55 +223,113 @@ __device__ __forceinline__ Place draw(const Chain &c, Place *lds) {
     return *lds;
 }
 
-template <int IO, bool CH, bool BETA>
+// What a wave has: R tokens from number `first` of the walk on, n of them inside the call.
+struct Part {
+    int b, c, n;
+    unsigned slab_c0;
+    bool on;         // lanes past the last channel repeat the last two and write nothing
+    long long first, row;  // row of the first token (of the last one of all, if none is inside)
+};
+__device__ __forceinline__ Part part_of(const GlrArgs &a, const Chain &chain, int slab, long long first, int R, int lane) {
+    const int C = a.H * a.d, per = chain.slabs / a.B;
+    Part p;
+    p.b = slab / per;
+    p.slab_c0 = slab % per * SLAB;
+    const int c = p.slab_c0 + 2 * lane;
+    p.on = c < C;
+    p.c = p.on ? c : C - 2;
+    p.first = first;
+    p.n = a.T - first >= R ? R : a.T > first ? (int)(a.T - first) : 0;
+    const long long i = p.n ? first : a.T - 1;
+    p.row = (long long)p.b * a.T + (a.reverse ? a.T - 1 - i : i);
+    return p;
+}
+
+// The R rows of one tensor, row by row from the first token; the rows past the end repeat the
+// last one.
+template <int R, typename F>
+__device__ __forceinline__ void each_row(const void *base, long long row_bytes, const Part &p, int reverse, F f) {
+    const char *at = static_cast<const char *>(base) + p.row * row_bytes;
+    const long long step = reverse ? -row_bytes : row_bytes;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        f(r, at);
+        if (r + 1 < p.n) at += step;
+    }
+}
+template <int R>
+__device__ __forceinline__ void load_gates(Gates<true, R> &g, const float *base, int C, const Part &p, int reverse, float past) {
+    each_row<R>(base, 4LL * C, p, reverse, [&](int r, const char *at) {
+        g.r[r] = *reinterpret_cast<const float2 *>(at + (unsigned)p.c * 4);
+    });
+    if (p.n < R)
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (r >= p.n) g.r[r] = make_float2(past, past);
+}
+template <int R, typename P>
+__device__ __forceinline__ void load_pairs(P (&v)[R], const void *base, int C, const Part &p, int reverse) {
+    each_row<R>(base, (long long)P::BYTES * C, p, reverse, [&](int r, const char *at) { v[r].load(at, p.c); });
+    if (p.n < R)
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (r >= p.n) v[r].zero();
+}
+
+template <int IO, bool CH, bool BETA, int R>
 __global__ __launch_bounds__(WAVES * LANES, 4) void glr_forward_kernel(GlrArgs a, Chain chain) {
-    constexpr int R = FWD_R;
     __shared__ float sA[WAVES][SLAB], sH[WAVES][SLAB], sC[SLAB];
+    __shared__ float sGa[Gates<CH, R>::STAGE], sGb[BETA ? Gates<CH, R>::STAGE : 1];
+    __shared__ Window window;
     __shared__ Place sP;
     const int lane = threadIdx.x % LANES, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / LANES), waves = blockDim.x / LANES;
     const Place at = draw(chain, &sP);
-    const int C = a.H * a.d, per = chain.slabs / a.B, b = at.slab / per;
-    const int c0 = at.slab % per * SLAB + 2 * lane;
-    const bool on = c0 < C;
-    const int c = on ? c0 : C - 2, h = c / a.d;  // lanes past the end repeat the last channels
-    const long long first = (long long)at.tile * (WAVES * R) + wave * R;
-    const long long base = (long long)b * a.T;
+    const int C = a.H * a.d;
+    const long long tile0 = (long long)at.tile * (WAVES * R);
+    const Part p = part_of(a, chain, at.slab, tile0 + wave * R, R, lane);
 
-    Gate<CH> ga[R], gb[R];
+    // Past the end a = 1 and b v = 0: the map that changes nothing.
+    Gates<CH, R> ga, gb;
     Pair<IO> v[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const long long i = first + r < a.T ? first + r : a.T - 1;
-        const size_t row = (size_t)(base + (a.reverse ? a.T - 1 - i : i));
-        ga[r].load(a.decay, row, C, a.H, c, h);
-        if (BETA) gb[r].load(a.beta, row, C, a.H, c, h);
-        v[r].load(a.v, row * C + c);
+    load_pairs<R>(v, a.v, C, p, a.reverse);
+    if constexpr (CH) {
+        load_gates<R>(ga, a.decay, C, p, a.reverse, 1.0f);
+        if (BETA) load_gates<R>(gb, a.beta, C, p, a.reverse, 0.0f);
+    } else {
+        ga.stage(sGa, a.decay, a, p.b, p.slab_c0, tile0, waves * R, 1.0f);
+        if (BETA) gb.stage(sGb, a.beta, a, p.b, p.slab_c0, tile0, waves * R, 0.0f);
+        ga.place(sGa, wave, lane, a.d);
+        if (BETA) gb.place(sGb, wave, lane, a.d);
+        __syncthreads();
     }
-    float2 x[R], A = {1.0f, 1.0f}, H = {0.0f, 0.0f};
+    // b v: per channel formed once (the gates' registers are free then), per head where it is used
+    float2 x[CH ? R : 1];
+    if constexpr (CH)
+#pragma unroll
+        for (int r = 0; r < R; ++r) x[r] = BETA ? mul2(gb.get(r), v[r].get()) : v[r].get();
+    auto input = [&](int r) { return CH ? x[CH ? r : 0] : BETA ? mul2(gb.get(r), v[r].get()) : v[r].get(); };
+    float2 A = {1.0f, 1.0f}, H = {0.0f, 0.0f};
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        x[r] = BETA ? mul2(gb[r].get(), v[r].get()) : v[r].get();
-        if (first + r >= a.T) {  // past the end: the map that changes nothing
-            ga[r].set(1.0f);
-            x[r] = {0.0f, 0.0f};
-        }
-        A = mul2(A, ga[r].get());
-        H = fma2(ga[r].get(), H, x[r]);
+        stretch(r);
+        A = mul2(A, ga.get(r));
+        H = fma2(ga.get(r), H, input(r));
     }
     lds2(sA[wave], lane) = A;
     lds2(sH[wave], lane) = H;
     __syncthreads();
     // the tile's map and start state, a channel per thread
+    const int share = CH ? 1 : a.d;  // channels with one decay
     for (int i = threadIdx.x; i < SLAB; i += blockDim.x) {
         float tA = sA[0][i], tH = sH[0][i], s = 0.0f;
         for (int w = 1; w < waves; ++w) {
             tH = fmaf(sA[w][i], tH, sH[w][i]);
             tA *= sA[w][i];
         }
-        const int ch = at.slab % per * SLAB + i;
-        const size_t st = (size_t)b * C + ch, wd = ((size_t)at.tile * chain.slabs + at.slab) * SLAB + i;
+        const int ch = p.slab_c0 + i;
+        const size_t st = (size_t)p.b * C + ch, wd = ((size_t)at.tile * chain.slabs + at.slab) * SLAB + i;
         if (at.tile > 0)
-            s = state_before(chain, at.call, at.tile, wd, tA, tH);
+            s = state_before(chain, window, i, at.call, at.tile, wd, wd - i % share, i % share == 0, tA, tH);
         else if (a.state_in && ch < C)
             s = a.state_in[st];
         const float e = fmaf(tA, s, tH);
@@ -244,18 +342,16 @@ __global__ __launch_bounds__(WAVES * LANES, 4) void glr_forward_kernel(GlrArgs a
     __syncthreads();
     float2 s = lds2(sC, lane);
     for (int w = 0; w < wave; ++w) s = fma2(lds2(sA[w], lane), s, lds2(sH[w], lane));
-    if (a.saved_out && on && first % GLR_TILE == 0 && first < a.T) {
-        const long long tiles = (a.T + GLR_TILE - 1) / GLR_TILE;
-        *reinterpret_cast<float2 *>(a.saved_out + ((size_t)b * tiles + first / GLR_TILE) * C + c) = s;
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        s = fma2(ga[r].get(), s, x[r]);
-        if (first + r < a.T && on) {
-            const size_t row = (size_t)(base + (a.reverse ? a.T - 1 - first - r : first + r));
-            OutPair<IO>::store(a.out, row * C + c, s);
-        }
-    }
+    const long long marks = (a.T + GLR_TILE - 1) / GLR_TILE;
+    if (!CH) anew(v);
+    each_row<R>(a.out, (long long)OutPair<IO>::BYTES * C, p, a.reverse, [&](int r, const char *row) {
+        stretch(r);
+        if (r >= p.n) return;
+        if (r % 16 == 0 && a.saved_out && (p.first + r) % GLR_TILE == 0 && p.on)
+            *reinterpret_cast<float2 *>(a.saved_out + ((size_t)p.b * marks + (p.first + r) / GLR_TILE) * C + p.c) = s;
+        s = fma2(ga.get(r), s, input(r));
+        if (p.on) OutPair<IO>::store(const_cast<char *>(row), p.c, s);
+    });
 }
 
 // Sums of N = 8 or 16 values over groups of L = 8, 16, 32 or 64 neighbouring lanes.  Each
@@ -284,65 +380,69 @@ __device__ __forceinline__ void group_sums(float (&v)[N], int L, int lane) {
     if (L >= 64) v[0] += __shfl_xor(v[0], 32);
 }
 
-template <int IO, bool CH, bool BETA>
+template <int IO, bool CH, bool BETA, int R>
 __global__ __launch_bounds__(WAVES * LANES, 4) void glr_backward_kernel(GlrArgs a, Chain chain) {
-    constexpr int R = BWD_R;
-    static_assert(WAVES * R == GLR_TILE, "a tile starts at a saved state");
+    static_assert(WAVES * R % GLR_TILE == 0 && GLR_TILE % R == 0 && R % 8 == 0, "a tile starts at a saved state");
     __shared__ float sA[WAVES][SLAB], sH[WAVES][SLAB], sG[WAVES][SLAB], sC[SLAB];
+    __shared__ float sGa[Gates<CH, R>::STAGE], sGb[BETA ? Gates<CH, R>::STAGE : 1];
+    __shared__ Window window;
     __shared__ Place sP;
     const int lane = threadIdx.x % LANES, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / LANES), waves = blockDim.x / LANES;
     const Place at = draw(chain, &sP);
-    const int C = a.H * a.d, per = chain.slabs / a.B, b = at.slab / per;
-    const int c0 = at.slab % per * SLAB + 2 * lane;
-    const bool on = c0 < C;
-    const int c = on ? c0 : C - 2, h = c / a.d;
+    const int C = a.H * a.d;
     const int tile = chain.tiles - 1 - at.tile;  // the gradient's walk: from the last tile to the first
-    const long long first = (long long)tile * (WAVES * R) + wave * R;
-    const long long base = (long long)b * a.T;
+    const long long tile0 = (long long)tile * (WAVES * R);
+    const Part p = part_of(a, chain, at.slab, tile0 + wave * R, R, lane);
 
-    Gate<CH> ga[R], gb[R];
+    // Past the end a = 1, b v = 0 and dout = 0: both maps change nothing.
+    Gates<CH, R> ga, gb;
     Pair<IO> v[R];
     OutPair<IO> dy[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const long long i = first + r < a.T ? first + r : a.T - 1;
-        const size_t row = (size_t)(base + (a.reverse ? a.T - 1 - i : i));
-        ga[r].load(a.decay, row, C, a.H, c, h);
-        if (BETA) gb[r].load(a.beta, row, C, a.H, c, h);
-        v[r].load(a.v, row * C + c);
-        dy[r].load(a.dout, row * C + c);
+    load_pairs<R>(v, a.v, C, p, a.reverse);
+    load_pairs<R>(dy, a.dout, C, p, a.reverse);
+    if constexpr (CH) {
+        load_gates<R>(ga, a.decay, C, p, a.reverse, 1.0f);
+        if (BETA) load_gates<R>(gb, a.beta, C, p, a.reverse, 0.0f);
+    } else {
+        ga.stage(sGa, a.decay, a, p.b, p.slab_c0, tile0, waves * R, 1.0f);
+        if (BETA) gb.stage(sGb, a.beta, a, p.b, p.slab_c0, tile0, waves * R, 0.0f);
+        ga.place(sGa, wave, lane, a.d);
+        if (BETA) gb.place(sGb, wave, lane, a.d);
+        __syncthreads();
     }
-    float2 s = *reinterpret_cast<const float2 *>(a.saved + ((size_t)b * chain.tiles + tile) * C + c);
-    auto input = [&](int r) { return BETA ? mul2(gb[r].get(), v[r].get()) : v[r].get(); };
+    // the saved state at or before this wave's first token
+    const long long marks = (a.T + GLR_TILE - 1) / GLR_TILE, mark = p.first / GLR_TILE < marks ? p.first / GLR_TILE : marks - 1;
+    float2 s = *reinterpret_cast<const float2 *>(a.saved + ((size_t)p.b * marks + mark) * C + p.c);
+    auto input = [&](int r) { return BETA ? mul2(gb.get(r), v[r].get()) : v[r].get(); };
     // the wave's maps: h -> A h + H forward, and backward c -> A c + G of c = a_{t+1} G_{t+1}
     float2 A = {1.0f, 1.0f}, H = {0.0f, 0.0f}, G = {0.0f, 0.0f};
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        if (first + r >= a.T) ga[r].set(1.0f);
-        const bool in = first + r < a.T;
-        A = mul2(A, ga[r].get());
-        H = fma2(ga[r].get(), H, in ? input(r) : make_float2(0.0f, 0.0f));
+        stretch(r);
+        A = mul2(A, ga.get(r));
+        H = fma2(ga.get(r), H, input(r));
     }
 #pragma unroll
-    for (int r = R - 1; r >= 0; --r)
-        if (first + r < a.T) {
-            const float2 d = dy[r].get();
-            G = mul2(ga[r].get(), make_float2(d.x + G.x, d.y + G.y));
-        }
+    for (int r = R - 1; r >= 0; --r) {
+        stretch(r);
+        const float2 d = dy[r].get();
+        G = mul2(ga.get(r), make_float2(d.x + G.x, d.y + G.y));
+    }
     lds2(sA[wave], lane) = A;
     lds2(sH[wave], lane) = H;
     lds2(sG[wave], lane) = G;
     __syncthreads();
+    const int share = CH ? 1 : a.d;
     for (int i = threadIdx.x; i < SLAB; i += blockDim.x) {
         float tA = 1.0f, tG = 0.0f, in = 0.0f;
         for (int w = waves - 1; w >= 0; --w) {
             tG = fmaf(sA[w][i], tG, sG[w][i]);
             tA *= sA[w][i];
         }
-        const int ch = at.slab % per * SLAB + i;
-        const size_t st = (size_t)b * C + ch, wd = ((size_t)at.tile * chain.slabs + at.slab) * SLAB + i;
+        const int ch = p.slab_c0 + i;
+        const size_t st = (size_t)p.b * C + ch, wd = ((size_t)at.tile * chain.slabs + at.slab) * SLAB + i;
         if (at.tile > 0)
-            in = state_before(chain, at.call, at.tile, wd, tA, tG);
+            in = state_before(chain, window, i, at.call, at.tile, wd, wd - i % share, i % share == 0, tA, tG);
         else if (a.dstate_out && ch < C)
             in = a.dstate_out[st];
         const float e = fmaf(tA, in, tG);
@@ -353,49 +453,64 @@ __global__ __launch_bounds__(WAVES * LANES, 4) void glr_backward_kernel(GlrArgs 
         sC[i] = in;
     }
     __syncthreads();
-    for (int w = 0; w < wave; ++w) s = fma2(lds2(sA[w], lane), s, lds2(sH[w], lane));
+    for (int w = wave / (GLR_TILE / R) * (GLR_TILE / R); w < wave; ++w) s = fma2(lds2(sA[w], lane), s, lds2(sH[w], lane));
     float2 g = lds2(sC, lane);
     for (int w = waves - 1; w > wave; --w) g = fma2(lds2(sA[w], lane), g, lds2(sG[w], lane));
-    float2 before[R];
+    anew(v);
+    anew(dy);
+    // the states before every fourth token; those between are formed again where they are
+    // used (a product more, 3/4 of the registers less)
+    float2 start[R / 4];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        before[r] = s;
-        s = fma2(ga[r].get(), s, input(r));
+        stretch(r);
+        if (r % 4 == 0) start[r / 4] = s;
+        s = fma2(ga.get(r), s, input(r));
     }
-    constexpr int N = BETA ? 2 * R : R;
-    float sum[N];  // per head: ddecay and dbeta of each token, this lane's two channels
+    anew(v);
+    const long long dir = a.reverse ? -1 : 1;
+    constexpr int N = BETA ? 16 : 8;
+    float sum[N];  // per head: ddecay and dbeta of eight tokens, this lane's two channels
 #pragma unroll
-    for (int r = R - 1; r >= 0; --r) {
-        const bool in = first + r < a.T;
-        const float2 d = dy[r].get(), x = v[r].get();
-        if (in) g = make_float2(d.x + g.x, d.y + g.y);
-        const float2 da = mul2(g, before[r]), db = mul2(g, x);
-        if (in && on) {
-            const size_t row = (size_t)(base + (a.reverse ? a.T - 1 - first - r : first + r));
-            if (a.dv) OutPair<IO>::store(a.dv, row * C + c, BETA ? mul2(gb[r].get(), g) : g);
-            if (CH && a.ddecay) *reinterpret_cast<float2 *>(a.ddecay + row * C + c) = da;
-            if (CH && BETA && a.dbeta) *reinterpret_cast<float2 *>(a.dbeta + row * C + c) = db;
+    for (int q = R / 4 - 1; q >= 0; --q) {
+        stretch(4 * q);
+        float2 before[4];
+        before[0] = start[q];
+#pragma unroll
+        for (int i = 1; i < 4; ++i) before[i] = fma2(ga.get(4 * q + i - 1), before[i - 1], input(4 * q + i - 1));
+#pragma unroll
+        for (int i = 3; i >= 0; --i) {
+            const int r = 4 * q + i;
+            const float2 d = dy[r].get(), x = v[r].get();
+            g = make_float2(d.x + g.x, d.y + g.y);
+            const float2 da = mul2(g, before[i]), db = mul2(g, x);
+            if (r < p.n && p.on) {
+                const size_t row = (size_t)(p.row + dir * r) * C;
+                if (a.dv)
+                    OutPair<IO>::store(static_cast<char *>(a.dv) + row * OutPair<IO>::BYTES, p.c, BETA ? mul2(gb.get(r), g) : g);
+                if (CH && a.ddecay) Pair<IO_F32>::store(reinterpret_cast<char *>(a.ddecay + row), p.c, da);
+                if (CH && BETA && a.dbeta) Pair<IO_F32>::store(reinterpret_cast<char *>(a.dbeta + row), p.c, db);
+            }
+            if (!CH) {
+                sum[r % 8] = da.x + da.y;
+                if constexpr (BETA) sum[8 + r % 8] = db.x + db.y;
+            }
+            g = mul2(ga.get(r), g);
         }
-        if (!CH) {
-            sum[r] = da.x + da.y;
-            if constexpr (BETA) sum[R + r] = db.x + db.y;
-        }
-        if (in) g = mul2(ga[r].get(), g);
-    }
-    if (!CH) {
-        const int L = a.d / 2, l = lane & (L - 1);
-        group_sums<N>(sum, L, lane);
-        auto put = [&](int i, float x) {
-            const int r = i & (R - 1);
-            float *to = BETA && i >= R ? a.dbeta : a.ddecay;
-            if (!to || !on || first + r >= a.T) return;
-            to[(size_t)(base + (a.reverse ? a.T - 1 - first - r : first + r)) * a.H + h] = x;
-        };
-        if (L == 8) {
-            put(l, sum[0]);
-            if constexpr (N == 16) put(8 + l, sum[1]);
-        } else if (l < N) {
-            put(l, sum[0]);
+        if (!CH && q % 2 == 0) {
+            const int L = a.d / 2, l = lane & (L - 1);
+            group_sums<N>(sum, L, lane);
+            auto put = [&](int i, float x) {
+                const int r = 4 * q + i % 8;
+                float *to = i >= 8 ? a.dbeta : a.ddecay;
+                if (to && p.on && r < p.n) to[(size_t)(p.row + dir * r) * a.H + p.c / a.d] = x;
+            };
+            if (L == 8) {
+                put(l, sum[0]);
+                if constexpr (N == 16) put(8 + l, sum[1]);
+            } else if (l < N) {
+                put(l, sum[0]);
+            }
         }
     }
 }
@@ -430,17 +545,37 @@ Chain chain_of(const GlrArgs &a, int tile) {
 // Waves of a block: a single tile of few tokens needs fewer.
 int waves_of(const GlrArgs &a, int R) { return (int)std::min<long long>(WAVES, (a.T + R - 1) / R); }
 
+// Long tiles only where calls have whole ones and they fill the device twice over (two
+// blocks fit on a CU): below that they leave waves or CUs idle.
+bool fills(const GlrArgs &a, int R) {
+    return a.T >= WAVES * R && slabs_of(a.B, a.H, a.d) * ((a.T + WAVES * R - 1) / (WAVES * R)) >= 2LL * a.ncu;
+}
+
+template <int IO, bool CH, bool BETA, int R>
+hipError_t forward_by(const GlrArgs &a, hipStream_t s) {
+    const Chain c = chain_of(a, WAVES * R);
+    glr_forward_kernel<IO, CH, BETA, R><<<dim3((unsigned)(c.slabs * c.tiles)), dim3(waves_of(a, R) * LANES), 0, s>>>(a, c);
+    return hipGetLastError();
+}
 template <int IO, bool CH, bool BETA>
 hipError_t forward(const GlrArgs &a, hipStream_t s) {
-    const Chain c = chain_of(a, WAVES * FWD_R);
-    glr_forward_kernel<IO, CH, BETA><<<dim3((unsigned)(c.slabs * c.tiles)), dim3(waves_of(a, FWD_R) * LANES), 0, s>>>(a, c);
+    constexpr int R = fwd_tokens(IO, CH);
+    if constexpr (R > 16)
+        if (fills(a, R)) return forward_by<IO, CH, BETA, R>(a, s);
+    return forward_by<IO, CH, BETA, 16>(a, s);
+}
+template <int IO, bool CH, bool BETA, int R>
+hipError_t backward_by(const GlrArgs &a, hipStream_t s) {
+    const Chain c = chain_of(a, WAVES * R);
+    glr_backward_kernel<IO, CH, BETA, R><<<dim3((unsigned)(c.slabs * c.tiles)), dim3(waves_of(a, R) * LANES), 0, s>>>(a, c);
     return hipGetLastError();
 }
 template <int IO, bool CH, bool BETA>
 hipError_t backward(const GlrArgs &a, hipStream_t s) {
-    const Chain c = chain_of(a, WAVES * BWD_R);
-    glr_backward_kernel<IO, CH, BETA><<<dim3((unsigned)(c.slabs * c.tiles)), dim3(waves_of(a, BWD_R) * LANES), 0, s>>>(a, c);
-    return hipGetLastError();
+    constexpr int R = bwd_tokens(IO, CH);
+    if constexpr (R > 8)
+        if (fills(a, R)) return backward_by<IO, CH, BETA, R>(a, s);
+    return backward_by<IO, CH, BETA, 8>(a, s);
 }
 
 // f<IO, per-channel gates, beta>(a, s) for the call's kind.

@@ -84,6 +84,13 @@ def test_long_and_wide(gate):
     parity("wide", lo.glr_inputs(15, 9, 140, 37, 128, gate))
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp8"])
+@pytest.mark.parametrize("d,H,beta", [(16, 64, True), (128, 8, False), (32, 33, True)])
+def test_long_tiles(dtype, d, H, beta):
+    """Enough channels and tokens for the long tiles of gates per head, with a ragged end."""
+    parity("long tiles", lo.glr_inputs(22, 16, 2345, H, d, "head", dtype, beta), dtype=dtype)
+
+
 @pytest.mark.parametrize("reverse", [False, True])
 def test_split_calls_carry_the_state_in_place(reverse):
     B, T, H, d = 2, 300, 3, 32
