@@ -65,7 +65,7 @@ struct GroupNormArgs {
     const void *dout;
     void *dx;
     float *dweight, *dbias;
-    long long N, S;
+    long long N, S, max_N;
     int C, G;
     int io;
     int silu;

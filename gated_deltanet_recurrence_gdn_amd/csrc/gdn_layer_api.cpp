@@ -221,7 +221,7 @@ int gn_check_sizes(gdn_ctx *h, long long N, long long S) {
 
 gdn::GroupNormArgs gn_args(const gdn_ctx *h, long long N, long long S) {
     gdn::GroupNormArgs a{};
-    a.N = N; a.S = S; a.C = h->gn.C; a.G = h->gn.G;
+    a.N = N; a.S = S; a.max_N = h->gn.max_N; a.C = h->gn.C; a.G = h->gn.G;
     a.io = h->gn.io_dtype; a.silu = h->gn.act == GDN_ACT_SILU; a.eps = h->gn.eps;
     a.work = h->work; a.ncu = h->ncu;
     return a;
