@@ -30,4 +30,62 @@ __device__ __forceinline__ void store1(void *p, size_t i, float x) {
         static_cast<uint16_t *>(p)[i] = (uint16_t)f32_to_bf16_bits(x);
 }
 
+// The output type that belongs to an input type.
+template <int IO>
+constexpr int OutIo = IO == IO_F32 ? IO_F32 : IO_BF16;
+
+// Address of element i.
+template <int IO>
+__device__ __forceinline__ const void *at(const void *p, size_t i) {
+    return static_cast<const char *>(p) + i * io_in_bytes(IO);
+}
+template <int IO>
+__device__ __forceinline__ void *at(void *p, size_t i) {
+    return static_cast<char *>(p) + i * io_in_bytes(IO);
+}
+
+// Eight neighbouring elements, as they lie in memory; i counts vectors.
+template <int IO>
+struct Vec;
+template <>
+struct Vec<IO_F32> {
+    float4 r[2];
+    __device__ __forceinline__ void load(const void *p, size_t i) {
+        r[0] = static_cast<const float4 *>(p)[2 * i];
+        r[1] = static_cast<const float4 *>(p)[2 * i + 1];
+    }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+        f[0] = r[0].x; f[1] = r[0].y; f[2] = r[0].z; f[3] = r[0].w;
+        f[4] = r[1].x; f[5] = r[1].y; f[6] = r[1].z; f[7] = r[1].w;
+    }
+    static __device__ __forceinline__ void store(void *p, size_t i, const float (&f)[8]) {
+        static_cast<float4 *>(p)[2 * i] = make_float4(f[0], f[1], f[2], f[3]);
+        static_cast<float4 *>(p)[2 * i + 1] = make_float4(f[4], f[5], f[6], f[7]);
+    }
+};
+template <>
+struct Vec<IO_BF16> {
+    uint4 r;
+    __device__ __forceinline__ void load(const void *p, size_t i) { r = static_cast<const uint4 *>(p)[i]; }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+        f[0] = bf16_lo(r.x); f[1] = bf16_hi(r.x); f[2] = bf16_lo(r.y); f[3] = bf16_hi(r.y);
+        f[4] = bf16_lo(r.z); f[5] = bf16_hi(r.z); f[6] = bf16_lo(r.w); f[7] = bf16_hi(r.w);
+    }
+    static __device__ __forceinline__ void store(void *p, size_t i, const float (&f)[8]) {
+        static_cast<uint4 *>(p)[i] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                                                pack_bf16x2(f[6], f[7]));
+    }
+};
+template <>
+struct Vec<IO_FP8> {
+    uint2 r;
+    __device__ __forceinline__ void load(const void *p, size_t i) { r = static_cast<const uint2 *>(p)[i]; }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+        fp8x4_to_f32(r.x, f);
+        fp8x4_to_f32(r.y, f + 4);
+    }
+};
+template <int IO>
+using OutVec = Vec<OutIo<IO>>;
+
 }  // namespace gdn
