@@ -8,8 +8,7 @@ namespace gdn {
 
 constexpr int ROTARY_MAX_PAIRS = 256;  // d <= 512
 
-// One rotary call.  Pair j (0 .. pairs-1, the sections' pairs one after another) has
-// turns[j] = theta^(-2i/dim) / 2 pi turns per unit of position on its axis.
+// One rotary call.  Pairs are numbered through the sections, 0 .. pairs-1.
 struct RotaryArgs {
     const void *x;
     void *out;
@@ -24,7 +23,7 @@ struct RotaryArgs {
     int halves, inverse;
     int dim[3];                            // section sizes
     int pairs;
-    double turns[ROTARY_MAX_PAIRS];
+    double log2_theta;
 };
 hipError_t launch_rotary(const RotaryArgs &a, hipStream_t stream);
 

@@ -283,11 +283,10 @@ int gdn_rotary(const gdn_rotary_config *cfg, const void *x, long long x_token_st
     a.B = c.B; a.H = c.H; a.d = c.d; a.T = T; a.io = c.io_dtype;
     a.halves = (c.flags & GDN_ROTARY_HALVES) != 0;
     a.inverse = (c.flags & GDN_ROTARY_INVERSE) != 0;
-    const double l = std::log2(c.theta);
+    a.log2_theta = std::log2(c.theta);
     for (int s = 0; s < 3; ++s) {
         a.dim[s] = c.axis_dim[s];
-        for (int i = 0; i < c.axis_dim[s] / 2; ++i)
-            a.turns[a.pairs++] = std::exp2(-2.0 * i / c.axis_dim[s] * l) * 0.15915494309189533577;  // 1 / 2 pi
+        a.pairs += c.axis_dim[s] / 2;
     }
     DeviceGuard g(c.device);
     st = launch_status(&ctx, gdn::launch_rotary(a, reinterpret_cast<hipStream_t>(hip_stream)), "rotary");

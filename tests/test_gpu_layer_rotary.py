@@ -24,7 +24,10 @@ def run_and_check(label, x, dims, got, positions, **how):
     (2, 3, 40, 128, (128, 0, 0)),
     (1, 4, 2, 96, (0, 0, 6)),
     (1, 130, 1, 16, (0, 0, 0)),        # nothing turns
-    (1, 70, 24, 128, (32, 48, 48)),    # sections of whole vectors
+    (1, 70, 24, 128, (32, 48, 48)),    # halves of eight, of four and of two elements
+    (2, 20, 3, 64, (16, 24, 24)),
+    (2, 20, 3, 64, (4, 20, 28)),
+    (3, 1400, 2, 32, (8, 8, 8)),       # several tokens a block, the last block not full
 ])
 def test_grid(dtype, halves, B, T, H, d, dims):
     x = lo.randn(lo.gen(1), B, T, H, d, dtype=dtype).cuda()
