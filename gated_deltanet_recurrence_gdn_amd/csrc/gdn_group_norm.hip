@@ -1,19 +1,19 @@
 // gdn_group_norm.hip -- group norm with an activation, channels last, and its gradient
 // (include/gdn.h, gdn_group_norm_forward / gdn_group_norm_backward).
 //
-// All forms are bound by HBM.  A thread holds eight neighbouring channels (a 16-byte vector
-// in bf16) and a fixed place in the row, so that weight and bias stay in registers; V = C / 8
-// threads make a row, and a block has R = threads / V rows at once.  Three forms by the size
-// of a sample:
+// All forms are bound by HBM, the small ones by the latency of their steps.  A thread holds
+// eight neighbouring channels (a 16-byte vector in bf16) and a fixed place in the row, so that
+// weight and bias stay in registers; V = C / 8 threads make a row, and a block has
+// R = threads / V rows at once.  Three forms by the size of a sample:
 //  * rows (S = 1, D = C / G channels of a group, D / 8 a power of two up to 64): a group is
 //    D / 8 lanes of a wave; its sums are exchanges between lanes and the row is read once.
-//  * resident (samples of up to RES_K vectors for each of 1024 threads): a block holds a
-//    sample in registers and joins its groups through LDS; one read, one launch.
+//  * resident (small samples): a block has a sample, in registers for the forward pass, and
+//    joins its groups through LDS; one launch.
 //  * split (larger samples): a sample is cut into stretches of rows.  One launch forms each
 //    stretch's sums, a small one joins them, one applies them, taking the stretches in the
 //    opposite order so that what the first left in the caches is read from there.
-// Squares are always taken around a mean: a thread's few rows around their own, and partial
-// results (count, mean, squares around it) are joined by
+// Squares are always taken around a mean, or a value of the set itself, and partial results
+// (count, mean, squares around it) are joined by
 //     mean = sum n_i mean_i / n,   squares = sum squares_i + sum n_i (mean_i - mean)^2,
 // so that means far from zero cost no precision.  Everything is fp32 until the last rounding.
 #include "gdn_elem.h"
@@ -24,7 +24,7 @@
 namespace gdn {
 namespace {
 
-constexpr int RES_K = 4;        // vectors of a thread in the resident form
+constexpr int RES_K = 4;        // rows of a thread in the resident form
 constexpr int ROWS_U = 4;       // rows a thread of the other forms has in flight
 constexpr int BATCH = 1024;     // samples of one round of the split form (bounds the workspace)
 
@@ -66,7 +66,8 @@ __device__ __forceinline__ void channel8(float (&f)[8], const float *p, int col,
     }
 }
 
-__device__ __forceinline__ float inv_std(float var, float eps) { return 1.0f / sqrtf(var + eps); }
+// eps is a normal number, which the hardware's reciprocal square root (an ulp) needs.
+__device__ __forceinline__ float inv_std(float var, float eps) { return __builtin_amdgcn_rsqf(var + eps); }
 
 // ---- rows ---------------------------------------------------------------------------
 
@@ -111,13 +112,17 @@ __global__ __launch_bounds__(512) void rows_forward_kernel(GroupNormArgs a, int 
     }
 }
 
+// Eight floats at the vector `i` of an LDS row.
+__device__ __forceinline__ void put8(float *lds, int i, const float (&f)[8]) {
+    reinterpret_cast<float4 *>(lds)[2 * i] = make_float4(f[0], f[1], f[2], f[3]);
+    reinterpret_cast<float4 *>(lds)[2 * i + 1] = make_float4(f[4], f[5], f[6], f[7]);
+}
+
 // Sums of a block's rows per channel: part[blockIdx.x][0 .. C) gets s1, [C .. 2C) s2.
 __device__ __forceinline__ void block_channels(const float (&s1)[8], const float (&s2)[8], float *lds, float *part, int C,
                                                int row, int col, int R) {
     for (int k = 0; k < 2; ++k) {
-        if (row < R)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) lds[row * C + 8 * col + i] = k ? s2[i] : s1[i];
+        if (row < R) put8(lds + row * C, col, k ? s2 : s1);
         __syncthreads();
         for (int c = threadIdx.x; c < C; c += blockDim.x) {
             float s = lds[c];
@@ -182,31 +187,129 @@ __global__ __launch_bounds__(512) void rows_backward_kernel(GroupNormArgs a, int
 
 // ---- joining a block's threads by group ---------------------------------------------
 
-// lds: R rows of C means, then R rows of C squares around them, of cnt(row) values each.  For
-// every group g calls done(g, count, mean, squares) (count: of `rows` rows) in one lane.  Several groups share a wave
-// where they are small.
-template <typename Count, typename Done>
-__device__ __forceinline__ void join_groups(const float *lds, int R, int C, int D, int rows, Count cnt, Done done) {
-    const float *mean = lds, *sq = lds + R * C;
-    const int items = R * D, G = C / D;
+// How many rows thread row r of R has of n: rows r, r + R, ...
+struct Share {
+    int each, extra;
+    __device__ __forceinline__ Share(int n, int R) : each(n / R), extra(n % R) {}
+    __device__ __forceinline__ float operator()(int r) const { return (float)(each + (r < extra)); }
+};
+
+// A thread's eight channels are first joined among themselves, as far as they are of one
+// group: `unit` channels, the largest of 8, 4, 2, 1 that divides D.  LDS then holds R rows of
+// C / unit entries (and R more for the second value).
+__device__ __forceinline__ int unit_of(int D) { return D % 8 == 0 ? 8 : D % 4 == 0 ? 4 : D % 2 == 0 ? 2 : 1; }
+
+template <int U>
+__device__ __forceinline__ void put_moments_by(float *lds, int R, int K, int row, int col, float count, const float (&mean)[8],
+                                               const float (&sq)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8 / U; ++e) {
+        float m = 0.0f, q = 0.0f;
+#pragma unroll
+        for (int i = 0; i < U; ++i) m += mean[e * U + i];
+        m *= 1.0f / U;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const float d = mean[e * U + i] - m;
+            q += fmaf(count * d, d, sq[e * U + i]);
+        }
+        lds[row * K + col * (8 / U) + e] = m;
+        lds[(R + row) * K + col * (8 / U) + e] = q;
+    }
+}
+__device__ __forceinline__ void put_moments(float *lds, int R, int C, int unit, int row, int col, float count,
+                                            const float (&mean)[8], const float (&sq)[8]) {
+    if (unit == 8)
+        put_moments_by<8>(lds, R, C / 8, row, col, count, mean, sq);
+    else if (unit == 4)
+        put_moments_by<4>(lds, R, C / 4, row, col, count, mean, sq);
+    else if (unit == 2)
+        put_moments_by<2>(lds, R, C / 2, row, col, count, mean, sq);
+    else
+        put_moments_by<1>(lds, R, C, row, col, count, mean, sq);
+}
+template <int U>
+__device__ __forceinline__ void put_sums_by(float *lds, int R, int K, int row, int col, const float (&s1)[8], const float (&s2)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8 / U; ++e) {
+        float a = 0.0f, b = 0.0f;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            a += s1[e * U + i];
+            b += s2[e * U + i];
+        }
+        lds[row * K + col * (8 / U) + e] = a;
+        lds[(R + row) * K + col * (8 / U) + e] = b;
+    }
+}
+__device__ __forceinline__ void put_sums(float *lds, int R, int C, int unit, int row, int col, const float (&s1)[8],
+                                         const float (&s2)[8]) {
+    if (unit == 8)
+        put_sums_by<8>(lds, R, C / 8, row, col, s1, s2);
+    else if (unit == 4)
+        put_sums_by<4>(lds, R, C / 4, row, col, s1, s2);
+    else if (unit == 2)
+        put_sums_by<2>(lds, R, C / 2, row, col, s1, s2);
+    else
+        put_sums_by<1>(lds, R, C, row, col, s1, s2);
+}
+
+// The whole block calls f(g, lane, L) for every group, L lanes of one wave for each (a power
+// of two up to 64, as many as a group has items if that is less); g >= G marks lanes that
+// only take part in the exchanges.
+template <typename F>
+__device__ __forceinline__ void each_group(int G, int items, F f) {
     int L = 1;
     while (L < 64 && L < items) L *= 2;
-    const int lane = threadIdx.x % L, per = blockDim.x / L;
-    const float total = (float)rows * (float)D;
-    for (int g0 = 0; g0 < G; g0 += per) {  // every lane of a wave stays for the exchanges
-        const int g = g0 + (int)threadIdx.x / L;
-        const int at = (g < G ? g : 0) * D;
+    const int per = blockDim.x / L;
+    for (int g0 = 0; g0 < G; g0 += per) f(g0 + (int)threadIdx.x / L, (int)threadIdx.x % L, L);
+}
+// i / n for 0 <= i < 2^16 with inv = 1 / n: the quotient's distance from a whole number is at
+// least 1 / 2n, its error below 2^-6 of that.
+__device__ __forceinline__ int quotient(int i, float inv) { return (int)(((float)i + 0.5f) * inv); }
+
+// What put_moments left: done(g, mean, squares) in one lane of each group of `rows` rows.
+template <typename Done>
+__device__ __forceinline__ void join_groups(const float *lds, int R, int C, int D, int unit, const Share &share, float rows,
+                                            Done done) {
+    const int K = C / unit, Du = D / unit, G = C / D, items = R * Du;
+    const float *mean = lds, *sq = lds + R * K;
+    const float inv = 1.0f / (float)Du, all = 1.0f / (rows * (float)Du);
+    each_group(G, items, [&](int g, int lane, int L) {
+        const int at = (g < G ? g : 0) * Du;
         float s = 0.0f, q = 0.0f;
-        for (int i = lane; i < items; i += L) s = fmaf(cnt(i / D), mean[i / D * C + at + i % D], s);
-        const float m = lanes_sum(s, L) / total;
         for (int i = lane; i < items; i += L) {
-            const int k = i / D * C + at + i % D;
+            const int r = quotient(i, inv);
+            s = fmaf(share(r), mean[r * K + at + i - r * Du], s);
+        }
+        const float m = lanes_sum(s, L) * all;
+        for (int i = lane; i < items; i += L) {
+            const int r = quotient(i, inv), k = r * K + at + i - r * Du;
             const float d = mean[k] - m;
-            q += fmaf(cnt(i / D) * d, d, sq[k]);
+            q += fmaf(share(r) * (float)unit * d, d, sq[k]);
         }
         q = lanes_sum(q, L);
-        if (g < G && lane == 0) done(g, total, m, q);
-    }
+        if (g < G && lane == 0) done(g, m, q);
+    });
+}
+
+// What put_sums left: done(g, sum1, sum2) in one lane of each group.
+template <typename Done>
+__device__ __forceinline__ void sum_groups(const float *lds, int R, int C, int D, int unit, Done done) {
+    const int K = C / unit, Du = D / unit, G = C / D, items = R * Du;
+    const float inv = 1.0f / (float)Du;
+    each_group(G, items, [&](int g, int lane, int L) {
+        const int at = (g < G ? g : 0) * Du;
+        float s1 = 0.0f, s2 = 0.0f;
+        for (int i = lane; i < items; i += L) {
+            const int r = quotient(i, inv), k = r * K + at + i - r * Du;
+            s1 += lds[k];
+            s2 += lds[R * K + k];
+        }
+        s1 = lanes_sum(s1, L);
+        s2 = lanes_sum(s2, L);
+        if (g < G && lane == 0) done(g, s1, s2);
+    });
 }
 
 // ---- resident -----------------------------------------------------------------------
@@ -219,7 +322,8 @@ __global__ __launch_bounds__(1024) void resident_forward_kernel(GroupNormArgs a,
     const int row = threadIdx.x / V, col = threadIdx.x % V, C = a.C, D = C / a.G, S = (int)a.S;
     const bool on = row < R;
     float2 *group = reinterpret_cast<float2 *>(lds + 2 * R * C);
-    auto cnt = [&](int r) { return (float)(r < S ? (S - r + R - 1) / R : 0); };
+    const Share share(S, R);
+    const int unit = unit_of(D);
     for (long long n = blockIdx.x; n < a.N; n += gridDim.x) {
         Vec<IO> x[RES_K];
         const size_t base = (size_t)n * S * V + col;
@@ -228,7 +332,7 @@ __global__ __launch_bounds__(1024) void resident_forward_kernel(GroupNormArgs a,
             if (on && row + k * R < S) x[k].load(a.x, base + (size_t)(row + k * R) * V);
         if (on) {
             float mean[8] = {}, sq[8] = {};
-            const float inv = row < S ? 1.0f / cnt(row) : 0.0f;
+            const float inv = row < S ? 1.0f / share(row) : 0.0f;
 #pragma unroll
             for (int k = 0; k < RES_K; ++k)
                 if (row + k * R < S) {
@@ -247,15 +351,11 @@ __global__ __launch_bounds__(1024) void resident_forward_kernel(GroupNormArgs a,
 #pragma unroll
                     for (int i = 0; i < 8; ++i) sq[i] = fmaf(f[i] - mean[i], f[i] - mean[i], sq[i]);
                 }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                lds[row * C + 8 * col + i] = mean[i];
-                lds[(R + row) * C + 8 * col + i] = sq[i];
-            }
+            put_moments(lds, R, C, unit, row, col, share(row), mean, sq);
         }
         __syncthreads();
-        join_groups(lds, R, C, D, S, cnt, [&](int g, float total, float mean, float sq) {
-            const float2 st = make_float2(mean, inv_std(sq / total, a.eps));
+        join_groups(lds, R, C, D, unit, share, (float)S, [&](int g, float mean, float sq) {
+            const float2 st = make_float2(mean, inv_std(sq / ((float)S * D), a.eps));
             group[g] = st;
             if (a.stats_out) reinterpret_cast<float2 *>(a.stats_out)[(size_t)n * a.G + g] = st;
         });
@@ -281,33 +381,14 @@ __global__ __launch_bounds__(1024) void resident_forward_kernel(GroupNormArgs a,
     }
 }
 
-// Sums over the rows and over a group's channels of two per-channel values: lds holds R rows
-// of C first values, then R rows of second ones; done(g, sum1, sum2) in one lane each.
-template <typename Done>
-__device__ __forceinline__ void sum_groups(const float *lds, int R, int C, int D, Done done) {
-    const int items = R * D, G = C / D;
-    int L = 1;
-    while (L < 64 && L < items) L *= 2;
-    const int lane = threadIdx.x % L, per = blockDim.x / L;
-    for (int g0 = 0; g0 < G; g0 += per) {
-        const int g = g0 + (int)threadIdx.x / L;
-        const int at = (g < G ? g : 0) * D;
-        float s1 = 0.0f, s2 = 0.0f;
-        for (int i = lane; i < items; i += L) {
-            s1 += lds[i / D * C + at + i % D];
-            s2 += lds[(R + i / D) * C + at + i % D];
-        }
-        s1 = lanes_sum(s1, L);
-        s2 = lanes_sum(s2, L);
-        if (g < G && lane == 0) done(g, s1, s2);
-    }
-}
-
+// The gradient reads a sample twice, the second time from the caches: x and dout in registers
+// beside the sums would spill.
 template <int IO, bool SILU>
 __global__ __launch_bounds__(1024) void resident_backward_kernel(GroupNormArgs a, int V, int R, float *part) {
     extern __shared__ float lds[];
     const int row = threadIdx.x / V, col = threadIdx.x % V, C = a.C, D = C / a.G, S = (int)a.S;
     const bool on = row < R;
+    const int unit = unit_of(D);
     float2 *group = reinterpret_cast<float2 *>(lds + 2 * R * C);
     const float inv = 1.0f / ((float)S * D);
     float w[8], b[8], sw[8] = {}, sb[8] = {};
@@ -316,60 +397,62 @@ __global__ __launch_bounds__(1024) void resident_backward_kernel(GroupNormArgs a
         channel8(b, a.bias, col, 0.0f);
     }
     for (long long n = blockIdx.x; n < a.N; n += gridDim.x) {
-        Vec<IO> x[RES_K];
-        OutVec<IO> y[RES_K];
         const size_t base = (size_t)n * S * V + col;
         float2 st[8];
         if (on) {
 #pragma unroll
-            for (int k = 0; k < RES_K; ++k)
-                if (row + k * R < S) {
-                    x[k].load(a.x, base + (size_t)(row + k * R) * V);
-                    y[k].load(a.dout, base + (size_t)(row + k * R) * V);
-                }
-#pragma unroll
             for (int i = 0; i < 8; ++i) st[i] = reinterpret_cast<const float2 *>(a.stats)[(size_t)n * a.G + (8 * col + i) / D];
             float s1[8] = {}, s2[8] = {};
+#pragma unroll 2
+            for (int r = row; r < S; r += R) {
+                Vec<IO> x;
+                OutVec<IO> y;
+                float f[8], t[8];
+                x.load(a.x, base + (size_t)r * V);
+                y.load(a.dout, base + (size_t)r * V);
+                x.get(f);
+                y.get(t);
 #pragma unroll
-            for (int k = 0; k < RES_K; ++k)
-                if (row + k * R < S) {
-                    float f[8], t[8];
-                    x[k].get(f);
-                    y[k].get(t);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float xh = (f[i] - st[i].x) * st[i].y, dz = act_grad<SILU>(t[i], fmaf(xh, w[i], b[i]));
-                        s1[i] += dz;
-                        s2[i] = fmaf(dz, xh, s2[i]);
-                    }
+                for (int i = 0; i < 8; ++i) {
+                    const float xh = (f[i] - st[i].x) * st[i].y, dz = act_grad<SILU>(t[i], fmaf(xh, w[i], b[i]));
+                    s1[i] += dz;
+                    s2[i] = fmaf(dz, xh, s2[i]);
                 }
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 sb[i] += s1[i];
                 sw[i] += s2[i];
-                lds[row * C + 8 * col + i] = s1[i] * w[i];
-                lds[(R + row) * C + 8 * col + i] = s2[i] * w[i];
+                s1[i] *= w[i];
+                s2[i] *= w[i];
             }
+            put_sums(lds, R, C, unit, row, col, s1, s2);
         }
         __syncthreads();
-        sum_groups(lds, R, C, D, [&](int g, float s1, float s2) { group[g] = make_float2(s1 * inv, s2 * inv); });
+        sum_groups(lds, R, C, D, unit, [&](int g, float s1, float s2) { group[g] = make_float2(s1 * inv, s2 * inv); });
         __syncthreads();
-        if (on && a.dx)
+        if (on && a.dx) {
+            float2 m[8];
 #pragma unroll
-            for (int k = 0; k < RES_K; ++k)
-                if (row + k * R < S) {
-                    float f[8], t[8];
-                    x[k].get(f);
-                    y[k].get(t);
+            for (int i = 0; i < 8; ++i) m[i] = group[(8 * col + i) / D];
+#pragma unroll 2
+            for (int r = row; r < S; r += R) {
+                Vec<IO> x;
+                OutVec<IO> y;
+                float f[8], t[8];
+                x.load(a.x, base + (size_t)r * V);
+                y.load(a.dout, base + (size_t)r * V);
+                x.get(f);
+                y.get(t);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 m = group[(8 * col + i) / D];
-                        const float xh = (f[i] - st[i].x) * st[i].y, dz = act_grad<SILU>(t[i], fmaf(xh, w[i], b[i]));
-                        t[i] = st[i].y * (dz * w[i] - m.x - xh * m.y);
-                    }
-                    OutVec<IO>::store(a.dx, base + (size_t)(row + k * R) * V, t);
+                for (int i = 0; i < 8; ++i) {
+                    const float xh = (f[i] - st[i].x) * st[i].y, dz = act_grad<SILU>(t[i], fmaf(xh, w[i], b[i]));
+                    t[i] = st[i].y * (dz * w[i] - m[i].x - xh * m[i].y);
                 }
-        __syncthreads();
+                OutVec<IO>::store(a.dx, base + (size_t)r * V, t);
+            }
+        }
+        __syncthreads();  // the next sample writes what is read above
     }
     if (part) block_channels(sb, sw, lds, part, C, row, col, R);
 }
@@ -383,86 +466,101 @@ struct Split {
 };
 
 // Mean and squares of one stretch and group: part[(n count + j) G + g].  grid: count, samples.
+// A thread takes its rows ROWS_U at a time, the next ones' loads issued before these are used.
+// Up to PIVOT_ROWS rows it sums the distances d from the first of them, p, and their squares:
+// p is in the set, so the squares around the set's mean are at least (p - mean)^2, and
+// sum d^2 - (sum d)^2 / n loses at most a factor n + 1 <= 33 of the last place.  Four
+// operations an element, where squares around running means take ten.
+constexpr int PIVOT_ROWS = 32;
 template <int IO>
 __global__ __launch_bounds__(1024) void split_stats_kernel(GroupNormArgs a, int V, int R, Split sp, long long n0, float2 *part) {
     extern __shared__ float lds[];
-    const int row = threadIdx.x / V, col = threadIdx.x % V, C = a.C;
-    const long long j = blockIdx.x, n = n0 + blockIdx.y;
-    const long long lo = j * sp.len, hi = lo + sp.len < a.S ? lo + sp.len : a.S;
+    const int row = threadIdx.x / V, col = threadIdx.x % V, C = a.C, D = C / a.G, unit = unit_of(D);
+    const long long j = blockIdx.x, n = n0 + blockIdx.y, lo = j * sp.len;
+    const int rows = (int)(lo + sp.len < a.S ? sp.len : a.S - lo);
+    const Share share(rows, R);
     if (row < R) {
-        float mean[8] = {}, sq[8] = {}, have = 0.0f;
-        const size_t base = (size_t)n * a.S * V + col;
-        long long r = lo + row;
-        // chunks of ROWS_U rows: around their own mean, then joined to those before
-        for (; r + (ROWS_U - 1) * R < hi; r += ROWS_U * R) {
-            Vec<IO> x[ROWS_U];
+        float mean[8] = {}, sq[8] = {}, p[8] = {}, s[8] = {}, q[8] = {};
+        const size_t base = ((size_t)n * a.S + lo) * V + col;
+        const int mine = row < rows ? (int)share(row) : 0;  // rows of this thread
+        Vec<IO> next[ROWS_U];
+        auto load = [&](int k) {  // number k of this thread's rows on; past the end the last again
 #pragma unroll
-            for (int u = 0; u < ROWS_U; ++u) x[u].load(a.x, base + (size_t)(r + u * R) * V);
+            for (int u = 0; u < ROWS_U; ++u) {
+                const int r = row + (k + u < mine ? k + u : mine - 1) * R;
+                next[u].load(a.x, base + (size_t)r * V);
+            }
+        };
+        auto join = [&](int before, int now) {  // `now` rows in p, s, q to `before` rows in mean, sq
+            const float k = (float)now, each = 1.0f / k, frac = k / (float)(before + now), weight = (float)before * frac;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float d = s[i] * each, m = p[i] + d, far = m - mean[i];
+                sq[i] += fmaf(far * far, weight, fmaxf(fmaf(-s[i], d, q[i]), 0.0f));
+                mean[i] = fmaf(far, frac, mean[i]);
+                s[i] = q[i] = 0.0f;
+            }
+        };
+        if (mine > 0) load(0);
+        int k = 0, from = 0;
+        for (; k < mine; k += ROWS_U) {
             float f[ROWS_U][8];
 #pragma unroll
-            for (int u = 0; u < ROWS_U; ++u) x[u].get(f[u]);
-            const float share = (float)ROWS_U / (have + ROWS_U), weight = have * share;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float m = 0.0f, q = 0.0f;
-#pragma unroll
-                for (int u = 0; u < ROWS_U; ++u) m += f[u][i];
-                m *= 1.0f / ROWS_U;
-#pragma unroll
-                for (int u = 0; u < ROWS_U; ++u) q = fmaf(f[u][i] - m, f[u][i] - m, q);
-                const float d = m - mean[i];
-                mean[i] = fmaf(d, share, mean[i]);
-                sq[i] += fmaf(d * d, weight, q);
+            for (int u = 0; u < ROWS_U; ++u) next[u].get(f[u]);
+            if (k + ROWS_U < mine) load(k + ROWS_U);
+            if (k - from == PIVOT_ROWS) {
+                join(from, PIVOT_ROWS);
+                from = k;
             }
-            have += ROWS_U;
-        }
-        for (; r < hi; r += R) {
-            Vec<IO> x;
-            float f[8];
-            x.load(a.x, base + (size_t)r * V);
-            x.get(f);
-            const float share = 1.0f / (have + 1.0f), weight = have * share;
+            if (k == from)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float d = f[i] - mean[i];
-                mean[i] = fmaf(d, share, mean[i]);
-                sq[i] = fmaf(d * d, weight, sq[i]);
-            }
-            have += 1.0f;
-        }
+                for (int i = 0; i < 8; ++i) p[i] = f[0][i];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            lds[row * C + 8 * col + i] = mean[i];
-            lds[(R + row) * C + 8 * col + i] = sq[i];
+            for (int u = 0; u < ROWS_U; ++u)
+                if (k + u < mine)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float d = f[u][i] - p[i];
+                        s[i] += d;
+                        q[i] = fmaf(d, d, q[i]);
+                    }
         }
+        if (mine > 0) join(from, mine - from);
+        put_moments(lds, R, C, unit, row, col, (float)mine, mean, sq);
     }
     __syncthreads();
-    const int rows = (int)(hi - lo);
-    join_groups(lds, R, C, C / a.G, rows, [&](int r) { return (float)(r < rows ? (rows - r + R - 1) / R : 0); },
-                [&](int g, float, float mean, float sq) {
-                    part[((size_t)blockIdx.y * sp.count + j) * a.G + g] = make_float2(mean, sq);
-                });
+    join_groups(lds, R, C, D, unit, share, (float)rows, [&](int g, float mean, float sq) {
+        part[((size_t)blockIdx.y * sp.count + j) * a.G + g] = make_float2(mean, sq);
+    });
 }
 
-// Joins a sample's stretches, a wave per sample and group: mean, 1 / std.
-__global__ __launch_bounds__(256) void split_stats_join_kernel(GroupNormArgs a, Split sp, int samples,
-                                                               const float2 *part, float2 *stats) {
-    const int lane = threadIdx.x % 64, D = a.C / a.G;
-    const long long id = (long long)blockIdx.x * 4 + threadIdx.x / 64;
-    if (id >= (long long)samples * a.G) return;
-    const int n = (int)(id / a.G), g = (int)(id % a.G);
+// Sum over the block's 256 threads, in each of them.
+__device__ __forceinline__ float block_sum(float x, float (&lds)[4]) {
+    x = lanes_sum(x, 64);
+    __syncthreads();
+    if (threadIdx.x % 64 == 0) lds[threadIdx.x / 64] = x;
+    __syncthreads();
+    return lds[0] + lds[1] + lds[2] + lds[3];
+}
+
+// Joins a sample's stretches, a block per group and sample: mean, 1 / std.
+__global__ __launch_bounds__(256) void split_stats_join_kernel(GroupNormArgs a, Split sp, const float2 *part, float2 *stats) {
+    __shared__ float lds[4];
+    const int g = blockIdx.x, n = blockIdx.y;
     const float2 *p = part + (size_t)n * sp.count * a.G + g;
-    const float total = (float)a.S * D;
-    auto cnt = [&](int j) { return (float)D * (float)(j + 1 < sp.count ? sp.len : a.S - j * sp.len); };
+    const float D = (float)(a.C / a.G), total = (float)a.S * D, full = (float)sp.len * D;
+    const float last = (float)(a.S - (sp.count - 1) * sp.len) * D;
     float s = 0.0f, q = 0.0f;
-    for (int j = lane; j < sp.count; j += 64) s = fmaf(cnt(j) / total, p[(size_t)j * a.G].x, s);
-    const float mean = lanes_sum(s, 64);
-    for (int j = lane; j < sp.count; j += 64) {
+#pragma unroll 4
+    for (int j = threadIdx.x; j < sp.count; j += 256) s = fmaf((j + 1 < sp.count ? full : last) / total, p[(size_t)j * a.G].x, s);
+    const float mean = block_sum(s, lds);
+#pragma unroll 4
+    for (int j = threadIdx.x; j < sp.count; j += 256) {
         const float2 v = p[(size_t)j * a.G];
-        q += fmaf(cnt(j) * (v.x - mean), v.x - mean, v.y);
+        q += fmaf((j + 1 < sp.count ? full : last) * (v.x - mean), v.x - mean, v.y);
     }
-    q = lanes_sum(q, 64);
-    if (lane == 0) stats[(size_t)n * a.G + g] = make_float2(mean, inv_std(q / total, a.eps));
+    q = block_sum(q, lds);
+    if (threadIdx.x == 0) stats[(size_t)n * a.G + g] = make_float2(mean, inv_std(q / total, a.eps));
 }
 
 template <int IO, bool SILU>
@@ -559,7 +657,7 @@ __global__ __launch_bounds__(1024) void split_dx_kernel(GroupNormArgs a, int V, 
     for (int c = threadIdx.x; c < 2 * C; c += blockDim.x)
         lds[c] = chan[(size_t)ny * 2 * C + c] * (a.weight ? a.weight[c < C ? c : c - C] : 1.0f);
     __syncthreads();
-    sum_groups(lds, 1, C, D, [&](int g, float s1, float s2) { group[g] = make_float2(s1 * inv, s2 * inv); });
+    sum_groups(lds, 1, C, D, 1, [&](int g, float s1, float s2) { group[g] = make_float2(s1 * inv, s2 * inv); });
     __syncthreads();
     if (row >= R) return;
     float w[8], b[8];
@@ -598,17 +696,20 @@ __global__ __launch_bounds__(1024) void split_dx_kernel(GroupNormArgs a, int V, 
     }
 }
 
-// Sums of the `rows` rows of part[blockIdx.y][rows][2][C] per channel: to[blockIdx.y][0 .. C)
-// first values and more[blockIdx.y][0 .. C) second ones (either may be nullptr), added to what
-// is there if `add`.  A block has 32 of the 2 C columns by 32 rows of threads.
-__global__ __launch_bounds__(1024) void channels_kernel(const float *part, int rows, int C, size_t pitch, float *first,
-                                                        float *second, int add) {
+// Sums of the rows of part [samples][rows][2][C] per channel.  Block row y < samples: the rows
+// of sample y, to chan[y][2][C].  The last block row (`whole`): all rows, to dbias and dweight
+// (either may be nullptr), added to what is there if `add`.  A block has 32 of the 2 C columns
+// by 32 rows of threads.
+__global__ __launch_bounds__(1024) void channels_kernel(const float *part, int samples, int rows, int C, float *chan, bool whole,
+                                                        float *dbias, float *dweight, bool add) {
     __shared__ float lds[32][33];
-    const int tc = threadIdx.x % 32, tr = threadIdx.x / 32, k = blockIdx.x * 32 + tc;
-    part += (size_t)blockIdx.y * rows * 2 * C;
+    const int tc = threadIdx.x % 32, tr = threadIdx.x / 32, k = blockIdx.x * 32 + tc, y = blockIdx.y;
+    const bool all = whole && y + 1 == (int)gridDim.y;
+    const size_t lo = all ? 0 : (size_t)y * rows, hi = all ? (size_t)samples * rows : lo + rows;
     float s = 0.0f;
     if (k < 2 * C)
-        for (int r = tr; r < rows; r += 32) s += part[(size_t)r * 2 * C + k];
+#pragma unroll 8
+        for (size_t r = lo + tr; r < hi; r += 32) s += part[r * 2 * C + k];
     lds[tr][tc] = s;
     __syncthreads();
     // column tr, its 32 partial sums across half a wave
@@ -616,9 +717,10 @@ __global__ __launch_bounds__(1024) void channels_kernel(const float *part, int r
     for (int l = 16; l > 0; l /= 2) s += __shfl_xor(s, l);
     const int c = blockIdx.x * 32 + tr;
     if (tc == 0 && c < 2 * C) {
-        float *to = c < C ? first : second;
-        if (to) {
-            to += blockIdx.y * pitch + (c < C ? c : c - C);
+        if (!all) {
+            chan[(size_t)y * 2 * C + c] = s;
+        } else if (float *to = c < C ? dbias : dweight) {
+            to += c < C ? c : c - C;
             *to = (add ? *to : 0.0f) + s;
         }
     }
@@ -642,6 +744,8 @@ bool rows_form(const GroupNormArgs &a) {
     const int D = a.C / a.G, P = D / 8;
     return a.S == 1 && D % 8 == 0 && (P & (P - 1)) == 0 && P <= 64 && a.C / 8 <= 512;
 }
+// At most RES_K rows of a thread.  A sample that fits is faster here than split even if it is
+// alone (3 x 77 x 320 fp32, forward and backward: 27 us, split 37 us: two launches more each).
 bool resident_form(const GroupNormArgs &a) { return a.S <= RES_K * (1024 / (a.C / 8)); }
 
 // Threads of the resident form: few for small samples, RES_K vectors each for large ones.
@@ -719,8 +823,7 @@ hipError_t forward(const GroupNormArgs &a, hipStream_t s) {
         const dim3 grid(sp.count, samples), block(l.threads);
         float2 *stats = a.stats_out ? reinterpret_cast<float2 *>(a.stats_out) + n0 * a.G : w.group;
         split_stats_kernel<IO><<<grid, block, lds, s>>>(a, l.V, l.R, sp, n0, reinterpret_cast<float2 *>(w.part));
-        split_stats_join_kernel<<<dim3((unsigned)(((long long)samples * a.G + 3) / 4)), dim3(256), 0, s>>>(
-            a, sp, samples, reinterpret_cast<const float2 *>(w.part), stats);
+        split_stats_join_kernel<<<dim3(a.G, samples), dim3(256), 0, s>>>(a, sp, reinterpret_cast<const float2 *>(w.part), stats);
         split_apply_kernel<IO, SILU><<<grid, block, 0, s>>>(a, l.V, l.R, sp, n0, stats);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
@@ -729,8 +832,8 @@ hipError_t forward(const GroupNormArgs &a, hipStream_t s) {
 }
 
 // dbias and dweight from `rows` rows of sums.
-hipError_t channels(const GroupNormArgs &a, const float *part, int rows, bool add, hipStream_t s) {
-    channels_kernel<<<dim3((2 * a.C + 31) / 32), dim3(1024), 0, s>>>(part, rows, a.C, 0, a.dbias, a.dweight, add);
+hipError_t channels(const GroupNormArgs &a, const float *part, int rows, hipStream_t s) {
+    channels_kernel<<<dim3((2 * a.C + 31) / 32), dim3(1024), 0, s>>>(part, 1, rows, a.C, nullptr, true, a.dbias, a.dweight, false);
     return hipGetLastError();
 }
 
@@ -738,13 +841,13 @@ template <int IO, bool SILU>
 hipError_t backward(const GroupNormArgs &a, hipStream_t s) {
     const bool wanted = a.dweight || a.dbias;
     const Work w = work_of(a);
-    if (a.N * a.S == 0) return wanted ? channels(a, w.part, 0, false, s) : hipSuccess;
+    if (a.N * a.S == 0) return wanted ? channels(a, w.part, 0, s) : hipSuccess;
     if (rows_form(a)) {
         const Layout l = layout(a.C, 256);
         const int blocks = (int)std::min<long long>((a.N + l.R - 1) / l.R, blocks_for(a.ncu, l.threads));
         rows_backward_kernel<IO, SILU><<<dim3(blocks), dim3(l.threads), (size_t)l.R * a.C * sizeof(float), s>>>(
             a, l.V, l.R, wanted ? w.part : nullptr);
-        return wanted ? channels(a, w.part, blocks, false, s) : hipGetLastError();
+        return wanted ? channels(a, w.part, blocks, s) : hipGetLastError();
     }
     if (resident_form(a)) {
         const Layout l = resident_layout(a);
@@ -753,7 +856,7 @@ hipError_t backward(const GroupNormArgs &a, hipStream_t s) {
         const hipError_t e = allow_lds(reinterpret_cast<const void *>(&resident_backward_kernel<IO, SILU>), lds);
         if (e != hipSuccess) return e;
         resident_backward_kernel<IO, SILU><<<dim3(blocks), dim3(l.threads), lds, s>>>(a, l.V, l.R, wanted ? w.part : nullptr);
-        return wanted ? channels(a, w.part, blocks, false, s) : hipGetLastError();
+        return wanted ? channels(a, w.part, blocks, s) : hipGetLastError();
     }
     const Layout l = layout(a.C, 256);
     const size_t lds = (size_t)l.R * a.C * sizeof(float);
@@ -764,11 +867,10 @@ hipError_t backward(const GroupNormArgs &a, hipStream_t s) {
         const Split sp = split_for(a, l, samples);
         const dim3 grid(sp.count, samples), block(l.threads);
         split_sums_kernel<IO, SILU><<<grid, block, lds, s>>>(a, l.V, l.R, sp, n0, w.part);
-        channels_kernel<<<dim3((2 * a.C + 31) / 32, samples), dim3(1024), 0, s>>>(w.part, sp.count, a.C, 2 * (size_t)a.C, w.chan,
-                                                                                 w.chan + a.C, 0);
+        channels_kernel<<<dim3((2 * a.C + 31) / 32, samples + wanted), dim3(1024), 0, s>>>(
+            w.part, samples, sp.count, a.C, w.chan, wanted, a.dbias, a.dweight, n0 > 0);
         if (a.dx) split_dx_kernel<IO, SILU><<<grid, block, dx_lds, s>>>(a, l.V, l.R, sp, n0, w.chan);
-        hipError_t e = hipGetLastError();
-        if (e == hipSuccess && wanted) e = channels(a, w.chan, samples, n0 > 0, s);
+        const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     return hipSuccess;

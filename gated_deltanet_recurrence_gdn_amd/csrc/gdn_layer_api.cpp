@@ -393,7 +393,7 @@ int gdn_group_norm_create(const gdn_group_norm_config *cfg, gdn_handle *out_h) {
         st = bad(GDN_ERR_UNSUPPORTED, "io_dtype = %d is not GDN_F32, GDN_BF16 or GDN_FP8", c.io_dtype);
     else if (c.act != GDN_ACT_NONE && c.act != GDN_ACT_SILU)
         st = bad(GDN_ERR_UNSUPPORTED, "act = %d is not GDN_ACT_NONE or GDN_ACT_SILU", c.act);
-    else if (!(c.eps > 0.0f) || !std::isfinite(c.eps)) st = bad(GDN_ERR_ARG, "eps must be > 0 and finite");
+    else if (!std::isnormal(c.eps) || c.eps < 0.0f) st = bad(GDN_ERR_ARG, "eps must be a positive normal number");
     else if (c.max_N < 0 || c.max_N > (1LL << 24))
         st = bad(GDN_ERR_ARG, "max_N = %lld must be from 0 to 2^24", c.max_N);
     if (st) return refused(fn, st);

@@ -382,7 +382,7 @@ typedef struct {
     int C, G;         /* channels, a multiple of 8 up to 8192, and groups; G divides C */
     int io_dtype;     /* gdn_dtype of x                                              */
     int act;          /* gdn_act                                                     */
-    float eps;        /* > 0 and finite                                              */
+    float eps;        /* a positive normal number                                    */
     long long max_N;  /* largest N any call on this handle will pass, 0 .. 2^24      */
 } gdn_group_norm_config;
 

@@ -139,7 +139,8 @@ def norm(C=64, Gn=4, io=gb.GDN_BF16, act=1, eps=1e-5, max_N=10, device=-1):
 
 @pytest.mark.parametrize("over,code", [
     (dict(C=60), UNSUP), (dict(C=0), UNSUP), (dict(C=8200), UNSUP), (dict(Gn=3), ARG), (dict(Gn=0), ARG), (dict(Gn=128), ARG),
-    (dict(io=9), UNSUP), (dict(act=2), UNSUP), (dict(eps=0.0), ARG), (dict(eps=float("nan")), ARG), (dict(max_N=-1), ARG),
+    (dict(io=9), UNSUP), (dict(act=2), UNSUP), (dict(eps=0.0), ARG),
+    (dict(eps=float("nan")), ARG), (dict(eps=1e-40), ARG), (dict(eps=-1e-5), ARG), (dict(eps=float("inf")), ARG), (dict(max_N=-1), ARG),
     (dict(max_N=(1 << 24) + 1), ARG), (dict(device=-2), ARG),
 ])
 def test_group_norm_create_refuses(over, code, capfd):
