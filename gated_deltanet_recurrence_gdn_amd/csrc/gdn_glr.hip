@@ -73,39 +73,42 @@ struct Window {
 __device__ float state_before(const Chain &c, Window &win, int i, uint32_t call, int k, size_t at, size_t mat, bool first,
                               float A, float H) {
     const size_t step = (size_t)c.slabs * SLAB;
+    const int lane = threadIdx.x % LANES, far = k < LOOK ? k : LOOK;
     post(c.add + at, word(call, H));
     if (first) post(c.mul + mat, word(call, A));
     for (;;) {
-        // the nearest known end state, four tiles at a time, with the maps behind it
-        float s = 0.0f;
-        int j = 0;
-        bool ok = true;
+        // Lane l asks for one word of the tile l + 1 back: whole rows of words in every
+        // round would fill the fabric that the tokens come through.
+        const u64 e = peek(c.end + at - lane - step * (lane < far ? lane + 1 : far));
+        const u64 found = __ballot(lane < far && (uint32_t)(e >> 32) == call);
+        if (found) {
+            // the nearest known end state, and the maps of the tiles behind it
+            const int j = __ffsll(found);
+            const u64 end = peek(c.end + at - step * j);
+            bool ok = true;
 #pragma unroll 1
-        for (int g = 0; g < LOOK && g < k && !j && ok; g += 4) {
-            u64 e[4], wm[4], wd[4];
+            for (int g = 1; g < j; g += 4) {
+                u64 wm[4], wd[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const size_t back = step * (g + q + 1 < k ? g + q + 1 : k);
-                e[q] = peek(c.end + at - back);
-                wm[q] = peek(c.mul + mat - back);
-                wd[q] = peek(c.add + at - back);
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                if (!j && ok) {
-                    if (known(e[q], call)) {
-                        j = g + q + 1;
-                        s = value(e[q]);
-                    }
-                    win.m[g + q][i] = value(wm[q]);
-                    win.d[g + q][i] = value(wd[q]);
-                    ok = g + q + 1 < k && known(wm[q], call) && known(wd[q], call);
+                for (int q = 0; q < 4; ++q) {
+                    const size_t back = step * (g + q < j ? g + q : j - 1);
+                    wm[q] = peek(c.mul + mat - back);
+                    wd[q] = peek(c.add + at - back);
                 }
-        }
-        if (j) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (g + q < j) {
+                        win.m[g + q - 1][i] = value(wm[q]);
+                        win.d[g + q - 1][i] = value(wd[q]);
+                        ok &= known(wm[q], call) && known(wd[q], call);
+                    }
+            }
+            if (ok && known(end, call)) {
+                float s = value(end);
 #pragma unroll 1
-            for (int q = j - 2; q >= 0; --q) s = fmaf(win.m[q][i], s, win.d[q][i]);
-            return s;
+                for (int q = j - 2; q >= 0; --q) s = fmaf(win.m[q][i], s, win.d[q][i]);
+                return s;
+            }
         }
         __builtin_amdgcn_s_sleep(1);
     }
