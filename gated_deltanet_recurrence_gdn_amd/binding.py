@@ -14,6 +14,7 @@ status.  ``GDN``, ``GLR`` and ``GroupNorm`` wrap a handle for torch callers, ``r
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -383,31 +384,41 @@ class GDN:
 _IO = {"bf16": GDN_BF16, "fp32": GDN_F32, "fp8": GDN_FP8}
 
 
-def _dtype_name(dtype):
-    """Name of a torch dtype that q, k, v, x may have."""
+def _io_of(dtype):
+    """gdn_dtype of a torch dtype that q, k, v, x may have."""
     import torch
-    names = {torch.bfloat16: "bf16", torch.float32: "fp32", torch.float8_e4m3fn: "fp8"}
-    if dtype not in names:
-        raise ValueError(f"expected bfloat16, float32 or float8_e4m3fn, got {dtype}")
-    return names[dtype]
+    if dtype is torch.bfloat16:
+        return GDN_BF16
+    if dtype is torch.float32:
+        return GDN_F32
+    if dtype is torch.float8_e4m3fn:
+        return GDN_FP8
+    raise ValueError(f"expected bfloat16, float32 or float8_e4m3fn, got {dtype}")
 
 
-def _expect(device, *tensors):
-    """Shape, dtype, layout and device of (name, tensor or None, shape, dtype): the C ABI takes
-    raw pointers and cannot know extents, so a wrong one is refused here."""
-    for name, x, shape, want in tensors:
-        if x is None:
-            continue
-        if tuple(x.shape) != tuple(shape) or x.dtype != want or not x.is_contiguous():
-            raise ValueError(f"{name}: expected contiguous {want} {tuple(shape)}, got {x.dtype} {tuple(x.shape)}")
-        if x.device.type != "cuda" or x.device.index != device:
-            raise ValueError(f"{name}: expected a tensor on cuda:{device}, got {x.device}")
+def _expect(device, name, x, shape, want):
+    """Shape, dtype, layout and device of a tensor (None passes): the C ABI takes raw pointers and
+    cannot know extents, so a wrong one is refused here."""
+    if x is None:
+        return
+    if x.shape != shape or x.dtype is not want or not x.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {want} {tuple(shape)}, got {x.dtype} {tuple(x.shape)}")
+    if x.get_device() != device or device < 0:  # host tensors say -1, as a dry-run handle does
+        raise ValueError(f"{name}: expected a tensor on cuda:{device}, got {x.device}")
 
 
 def _stream_of(device: int):
-    """The raw hipStream_t of torch's current stream on that device (not of the current device's)."""
+    """The raw hipStream_t of torch's current stream on that device (not of the current device's).
+    torch's own accessor for launchers; torch.cuda.current_stream wraps the same value in an object,
+    a microsecond that a call on one token feels."""
     import torch
-    return torch.cuda.current_stream(device).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
+@functools.lru_cache(maxsize=256)
+def _rotary_config(*values):
+    device, B, H, d, io, dims, theta, flags = values
+    return gdn_rotary_config(device, B, H, d, io, (ctypes.c_int * 3)(*dims), theta, flags)
 
 
 def rotary(x, axis_dims, theta=10000.0, positions=None, grid=None, first_token=0, halves=False, inverse=False,
@@ -421,23 +432,31 @@ def rotary(x, axis_dims, theta=10000.0, positions=None, grid=None, first_token=0
     gradient with respect to x.  out may be x (in place).  Returns out (fp32 for fp32 x, else bf16).
     """
     import torch
-    io = _IO[_dtype_name(x.dtype)]
+    io = _io_of(x.dtype)
     odt = torch.float32 if io == GDN_F32 else torch.bfloat16
-    if x.dim() != 4 or x.device.type != "cuda":
+    device = x.get_device()
+    if x.dim() != 4 or device < 0:
         raise ValueError(f"x: expected a [B, T, H, d] tensor on a GPU, got {tuple(x.shape)} on {x.device}")
     B, T, H, d = x.shape
     if out is None:
         out = torch.empty((B, T, H, d), dtype=odt, device=x.device)
-    elif tuple(out.shape) != (B, T, H, d) or out.dtype != odt or out.device != x.device:
+    elif out.shape != x.shape or out.dtype is not odt or out.get_device() != device:
         raise ValueError(f"out: expected {odt} {(B, T, H, d)} on {x.device}, got {out.dtype} {tuple(out.shape)}")
-    if 0 in (B, H, d) or T == 0:
+    if 0 in (B, H, d, T):
         return out
-    for name, y in (("x", x), ("out", out)):
-        if (d > 1 and y.stride(3) != 1) or (H > 1 and y.stride(2) != d):
-            raise ValueError(f"{name}: the heads of a token must lie side by side, got strides {y.stride()}")
+    xbs, xts, xhs, xes = x.stride()
+    obs, ots, ohs, oes = out.stride()
+    for name, hs, es in (("x", xhs, xes), ("out", ohs, oes)):
+        if (d > 1 and es != 1) or (H > 1 and hs != d):
+            raise ValueError(f"{name}: the heads of a token must lie side by side, got strides "
+                             f"{(x if name == 'x' else out).stride()}")
+    if T == 1:  # a dimension of one has no stride of its own
+        xts = ots = H * d
+    if B == 1:
+        xbs = obs = 0
     pbs = 0
     if positions is not None:
-        if positions.dtype != torch.int32 or positions.device != x.device or not positions.is_contiguous() or \
+        if positions.dtype is not torch.int32 or positions.get_device() != device or not positions.is_contiguous() or \
                 tuple(positions.shape) not in ((T, 3), (B, T, 3)):
             raise ValueError(f"positions: expected contiguous int32 {(T, 3)} or {(B, T, 3)} on {x.device}, "
                              f"got {positions.dtype} {tuple(positions.shape)} on {positions.device}")
@@ -448,14 +467,9 @@ def rotary(x, axis_dims, theta=10000.0, positions=None, grid=None, first_token=0
         raise ValueError("positions or grid must be given")
     else:
         height, width = grid
-    dt, dy, dx = axis_dims
     flags = (GDN_ROTARY_HALVES if halves else 0) | (GDN_ROTARY_INVERSE if inverse else 0)
-    cfg = gdn_rotary_config(x.device.index, B, H, d, io, (ctypes.c_int * 3)(dt, dy, dx), theta, flags)
-    # a dimension of one has no stride of its own
-    xts, ots = (y.stride(1) if T > 1 else H * d for y in (x, out))
-    xbs, obs = (y.stride(0) if B > 1 else 0 for y in (x, out))
-    st = gdn_rotary(cfg, x, xts, xbs, out, ots, obs, positions, pbs, first_token, height, width, T,
-                    _stream_of(x.device.index))
+    cfg = _rotary_config(device, B, H, d, io, tuple(axis_dims), float(theta), flags)
+    st = gdn_rotary(cfg, x, xts, xbs, out, ots, obs, positions, pbs, first_token, height, width, T, _stream_of(device))
     if st != GDN_OK:
         raise GDNError(st, gdn_last_error(None))
     return out
@@ -490,11 +504,12 @@ class _Handle:
         if st != GDN_OK:
             raise GDNError(st, gdn_last_error(self.h))
 
-    def _torch_types(self, dtype):
-        """(dtype of the input, dtype of the outputs): outputs are fp32 for fp32 inputs, bf16 otherwise."""
+    def _set_types(self, dtype):
+        """The dtype of the input, and of the outputs: fp32 for fp32 inputs, bf16 otherwise."""
         import torch
-        return {"bf16": (torch.bfloat16, torch.bfloat16), "fp32": (torch.float32, torch.float32),
-                "fp8": (torch.float8_e4m3fn, torch.bfloat16)}[dtype]
+        self._f32 = torch.float32
+        self._in, self._out = {"bf16": (torch.bfloat16, torch.bfloat16), "fp32": (torch.float32, torch.float32),
+                               "fp8": (torch.float8_e4m3fn, torch.bfloat16)}[dtype]
 
 
 class GLR(_Handle):
@@ -505,37 +520,37 @@ class GLR(_Handle):
     def __init__(self, B, H, d, dtype="bf16", max_T=0, device=0, gate="head", reverse=False):
         self.B, self.H, self.d, self.dtype, self.device = B, H, d, dtype, device
         self.gate_dim = {"head": 1, "channel": d}[gate]
+        self._set_types(dtype)
+        self._state = (B, H, d)
         self._open(gdn_glr_create(device, B, H, d, _IO[dtype], self.gate_dim, max_T,
                                   GDN_FLAG_REVERSE if reverse else 0))
 
-    def _shapes(self, T):
-        B, H, d = self.B, self.H, self.d
-        tok = (B, T, H, d)
-        return tok, ((B, T, H) if self.gate_dim == 1 else tok), (B, H, d), (B, -(-T // GDN_GLR_SAVED_TOKENS), H, d)
-
     def _inputs(self, v, beta, decay):
-        import torch
+        """(T, shape of v, shape of the gates)"""
         if v.dim() != 4:
             raise ValueError(f"v: expected [B, T, H, d], got {tuple(v.shape)}")
         T = v.shape[1]
-        tok, gate, _, _ = self._shapes(T)
-        dt, _ = self._torch_types(self.dtype)
-        _expect(self.device, ("v", v, tok, dt), ("beta", beta, gate, torch.float32),
-                ("decay", decay, gate, torch.float32))
-        return T
+        tok = (self.B, T, self.H, self.d)
+        gate = tok[:3] if self.gate_dim == 1 else tok
+        _expect(self.device, "v", v, tok, self._in)
+        _expect(self.device, "beta", beta, gate, self._f32)
+        _expect(self.device, "decay", decay, gate, self._f32)
+        return T, tok, gate
 
-    def _forward(self, v, beta, decay, state_in, state_out, out, return_state, saved):
+    def _saved(self, T):
+        return (self.B, -(-T // GDN_GLR_SAVED_TOKENS), self.H, self.d)
+
+    def _forward(self, v, beta, decay, state_in, state_out, out, return_state, save):
         import torch
-        T = self._inputs(v, beta, decay)
-        tok, _, st, sv = self._shapes(T)
-        _, odt = self._torch_types(self.dtype)
-        f32 = torch.float32
-        _expect(self.device, ("state_in", state_in, st, f32), ("state_out", state_out, st, f32), ("out", out, tok, odt))
+        T, tok, _ = self._inputs(v, beta, decay)
+        _expect(self.device, "state_in", state_in, self._state, self._f32)
+        _expect(self.device, "state_out", state_out, self._state, self._f32)
+        _expect(self.device, "out", out, tok, self._out)
         if out is None:
-            out = torch.empty(tok, dtype=odt, device=v.device)
+            out = torch.empty(tok, dtype=self._out, device=v.device)
         if state_out is None and return_state:
-            state_out = torch.empty(st, dtype=f32, device=v.device)
-        saved = torch.empty(sv, dtype=f32, device=v.device) if saved else None
+            state_out = torch.empty(self._state, dtype=self._f32, device=v.device)
+        saved = torch.empty(self._saved(T), dtype=self._f32, device=v.device) if save else None
         self._check(gdn_glr_forward(self.h, v, beta, decay, state_in, state_out, saved, out, T,
                                     _stream_of(self.device)))
         return out, state_out, saved
@@ -552,15 +567,14 @@ class GLR(_Handle):
         """The gradient of ``forward_train`` at the same v, beta, decay and its saved.  Returns
         (dv, dbeta, ddecay, dstate_in); dbeta is None without beta."""
         import torch
-        T = self._inputs(v, beta, decay)
-        tok, gate, st, sv = self._shapes(T)
-        _, odt = self._torch_types(self.dtype)
-        f32 = torch.float32
-        _expect(self.device, ("saved", saved, sv, f32), ("dout", dout, tok, odt), ("dstate_out", dstate_out, st, f32))
-        dv = torch.empty(tok, dtype=odt, device=v.device)
-        dbeta = None if beta is None else torch.empty(gate, dtype=f32, device=v.device)
-        ddecay = torch.empty(gate, dtype=f32, device=v.device)
-        dstate_in = torch.empty(st, dtype=f32, device=v.device)
+        T, tok, gate = self._inputs(v, beta, decay)
+        _expect(self.device, "saved", saved, self._saved(T), self._f32)
+        _expect(self.device, "dout", dout, tok, self._out)
+        _expect(self.device, "dstate_out", dstate_out, self._state, self._f32)
+        dv = torch.empty(tok, dtype=self._out, device=v.device)
+        dbeta = None if beta is None else torch.empty(gate, dtype=self._f32, device=v.device)
+        ddecay = torch.empty(gate, dtype=self._f32, device=v.device)
+        dstate_in = torch.empty(self._state, dtype=self._f32, device=v.device)
         self._check(gdn_glr_backward(self.h, v, beta, decay, saved, dout, dstate_out, dv, dbeta, ddecay, dstate_in, T,
                                      _stream_of(self.device)))
         return dv, dbeta, ddecay, dstate_in
@@ -573,30 +587,30 @@ class GroupNorm(_Handle):
 
     def __init__(self, C, G, dtype="bf16", act="silu", eps=1e-5, max_N=1, device=0):
         self.C, self.G, self.dtype, self.device = C, G, dtype, device
+        self._set_types(dtype)
         self._open(gdn_group_norm_create(device, C, G, _IO[dtype], {"none": GDN_ACT_NONE, "silu": GDN_ACT_SILU}[act],
                                          eps, max_N))
 
     def _inputs(self, x, weight, bias):
-        import torch
-        dt, _ = self._torch_types(self.dtype)
         if x.dim() < 2:
             raise ValueError(f"x: expected [N, ..., C], got {tuple(x.shape)}")
-        N, S = x.shape[0], 1
-        for n in x.shape[1:-1]:
+        shape = x.shape
+        N, S = shape[0], 1
+        for n in shape[1:-1]:
             S *= n
-        _expect(self.device, ("x", x, (*x.shape[:-1], self.C), dt), ("weight", weight, (self.C,), torch.float32),
-                ("bias", bias, (self.C,), torch.float32))
+        _expect(self.device, "x", x, (*shape[:-1], self.C), self._in)
+        _expect(self.device, "weight", weight, (self.C,), self._f32)
+        _expect(self.device, "bias", bias, (self.C,), self._f32)
         return N, S
 
     def forward(self, x, weight=None, bias=None, out=None, return_stats=True):
         """Returns (out, stats); stats [N, G, 2] (mean, 1 / sqrt(var + eps)) goes to ``backward``."""
         import torch
         N, S = self._inputs(x, weight, bias)
-        _, odt = self._torch_types(self.dtype)
-        _expect(self.device, ("out", out, x.shape, odt))
+        _expect(self.device, "out", out, x.shape, self._out)
         if out is None:
-            out = torch.empty(x.shape, dtype=odt, device=x.device)
-        stats = torch.empty((N, self.G, 2), dtype=torch.float32, device=x.device) if return_stats else None
+            out = torch.empty(x.shape, dtype=self._out, device=x.device)
+        stats = torch.empty((N, self.G, 2), dtype=self._f32, device=x.device) if return_stats else None
         self._check(gdn_group_norm_forward(self.h, x, weight, bias, out, stats, N, S, _stream_of(self.device)))
         return out, stats
 
@@ -605,9 +619,9 @@ class GroupNorm(_Handle):
         dbias); dweight and dbias are None without weight and bias."""
         import torch
         N, S = self._inputs(x, weight, bias)
-        _, odt = self._torch_types(self.dtype)
-        _expect(self.device, ("stats", stats, (N, self.G, 2), torch.float32), ("dout", dout, x.shape, odt))
-        dx = torch.empty(x.shape, dtype=odt, device=x.device)
+        _expect(self.device, "stats", stats, (N, self.G, 2), self._f32)
+        _expect(self.device, "dout", dout, x.shape, self._out)
+        dx = torch.empty(x.shape, dtype=self._out, device=x.device)
         dweight = None if weight is None else torch.empty_like(weight)
         dbias = None if bias is None else torch.empty_like(bias)
         self._check(gdn_group_norm_backward(self.h, x, weight, bias, stats, dout, dx, dweight, dbias, N, S,

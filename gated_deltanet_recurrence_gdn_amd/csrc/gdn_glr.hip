@@ -357,6 +357,29 @@ __global__ __launch_bounds__(WAVES * LANES, 4) void glr_forward_kernel(GlrArgs a
     });
 }
 
+// One token: a lane has two channels, and nothing is joined.  The same fused product and sum
+// as a tile's, so a token on its own gives the bits that it gives as a tile of one.
+template <int IO, bool CH, bool BETA>
+__global__ __launch_bounds__(256) void glr_step_kernel(GlrArgs a) {
+    const unsigned i = 2 * (blockIdx.x * 256 + threadIdx.x);  // channel of the batch
+    if (i >= (unsigned)a.B * a.H * a.d) return;
+    const char *v = static_cast<const char *>(a.v);
+    Pair<IO> x;
+    x.load(v, i);
+    const unsigned head = i / (unsigned)a.d;
+    auto gate = [&](const float *p) {
+        return CH ? *reinterpret_cast<const float2 *>(p + i) : make_float2(p[head], p[head]);
+    };
+    float2 s = {0.0f, 0.0f}, in = x.get();
+    if (a.state_in) s = *reinterpret_cast<const float2 *>(a.state_in + i);
+    const float2 A = gate(a.decay);
+    if (BETA) in = mul2(gate(a.beta), in);
+    if (a.saved_out) *reinterpret_cast<float2 *>(a.saved_out + i) = s;
+    s = fma2(A, s, in);
+    if (a.state_out) *reinterpret_cast<float2 *>(a.state_out + i) = s;
+    OutPair<IO>::store(static_cast<char *>(a.out), i, s);
+}
+
 // Sums of N = 8 or 16 values over groups of L = 8, 16, 32 or 64 neighbouring lanes.  Each
 // step sends half of a lane's values to a partner and adds the partner's other half: N - 1
 // moves for N = 16 instead of N log2 L.  Afterwards lane l of a group has value
@@ -562,6 +585,11 @@ hipError_t forward_by(const GlrArgs &a, hipStream_t s) {
 }
 template <int IO, bool CH, bool BETA>
 hipError_t forward(const GlrArgs &a, hipStream_t s) {
+    if (a.T == 1) {
+        const long long lanes = (long long)a.B * a.H * a.d / 2;  // at most 2^28 channels: B * slabs is below 2^22
+        glr_step_kernel<IO, CH, BETA><<<dim3((unsigned)((lanes + 255) / 256)), dim3(256), 0, s>>>(a);
+        return hipGetLastError();
+    }
     constexpr int R = fwd_tokens(IO, CH);
     if constexpr (R > 16)
         if (fills(a, R)) return forward_by<IO, CH, BETA, R>(a, s);
