@@ -90,8 +90,8 @@ int check_device(int device, int *ncu) {
     return GDN_OK;
 }
 
-// A new handle of `kind` with `bytes` of device workspace; on failure one line on stderr.
-int make_handle(int kind, int device, size_t bytes, gdn_ctx **out) {
+// A new handle of `kind` with `bytes` of device workspace, set to zero if asked for.
+int make_handle(int kind, int device, size_t bytes, bool zeroed, gdn_ctx **out) {
     int ncu = 0;
     void *work = nullptr;
     if (device >= 0) {
@@ -99,7 +99,7 @@ int make_handle(int kind, int device, size_t bytes, gdn_ctx **out) {
         if (bytes) {
             DeviceGuard g(device);
             hipError_t e = hipMalloc(&work, bytes);
-            if (e == hipSuccess) {  // workspaces start zeroed
+            if (e == hipSuccess && zeroed) {
                 e = hipMemset(work, 0, bytes);
                 if (e == hipSuccess) e = hipStreamSynchronize(nullptr);
                 if (e != hipSuccess) (void)hipFree(work);
@@ -316,7 +316,7 @@ int gdn_glr_create(const gdn_glr_config *cfg, gdn_handle *out_h) {
         st = bad(GDN_ERR_UNSUPPORTED, "B * ceil(H d / 128) * ceil(max_T / %d) exceeds 2^22", gdn::GLR_TILE);
     if (st) return refused(fn, st);
     gdn_ctx *h = nullptr;
-    if ((st = make_handle(KIND_GLR, c.device, gdn::glr_work_bytes(c.B, c.H, c.d, c.max_T), &h))) return refused(fn, st);
+    if ((st = make_handle(KIND_GLR, c.device, gdn::glr_work_bytes(c.B, c.H, c.d, c.max_T), true, &h))) return refused(fn, st);
     h->glr = c;
     *out_h = h;
     return GDN_OK;
@@ -398,7 +398,7 @@ int gdn_group_norm_create(const gdn_group_norm_config *cfg, gdn_handle *out_h) {
         st = bad(GDN_ERR_ARG, "max_N = %lld must be from 0 to 2^24", c.max_N);
     if (st) return refused(fn, st);
     gdn_ctx *h = nullptr;
-    if ((st = make_handle(KIND_GROUP_NORM, c.device, gdn::group_norm_work_bytes(c.C, c.G, c.max_N), &h)))
+    if ((st = make_handle(KIND_GROUP_NORM, c.device, gdn::group_norm_work_bytes(c.C, c.G, c.max_N), false, &h)))
         return refused(fn, st);
     h->gn = c;
     *out_h = h;

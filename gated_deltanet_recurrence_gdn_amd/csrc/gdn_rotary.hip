@@ -3,12 +3,18 @@
 // Bound by HBM: six flops per pair read and written.  Pair j of every head of a token is
 // turned by the same angle, so a block takes TOK tokens at a time, forms their cosines and
 // sines once (frequency and angle in 64 bits, the angle reduced to a fraction of a turn before
-// the fp32 sine) into LDS and turns all heads with them.
+// the fp32 sine) into LDS and turns all heads with them.  The frequencies are formed once a
+// block; blocks stay for many tokens.
 //  * pairs (2i, 2i + 1): a lane takes eight neighbouring elements (16 bytes of bf16), four
 //    whole pairs.
-//  * halves: a lane takes W neighbouring elements of a section's first half and the W of the
-//    second half that belong to them; W is the largest of 8, 4, 2, 1 that divides every half.
-// A pair is read and written by one lane, so out may be x.
+//  * halves that are multiples of W elements, W * size >= 8 bytes: a lane takes W neighbouring
+//    elements of a section's first half and the W of the second half that belong to them.
+//  * other halves: whole heads are staged in LDS in 16-byte vectors; a lane forms eight
+//    neighbouring outputs and finds their partners there.  (Two-byte accesses to memory
+//    instead: 1.3 TB/s where this has
+//    2.9 TB/s, at 2 x 11,267 tokens of 26 heads of 64 in bf16.)
+// out may be x: a pair is read and written by one lane, and heads are staged whole before any
+// of them is written.
 #include "gdn_elem.h"
 #include "gdn_layer.h"
 
@@ -18,72 +24,64 @@ namespace gdn {
 namespace {
 
 constexpr int THREADS = 256;
+constexpr int ROTARY_BLOCKS = 1 << 14;
 
-// The angle of pair j of token t of batch element b, in turns, less whole turns.
-__device__ __forceinline__ float part_turn(const RotaryArgs &a, unsigned b, long long t, int j) {
-    int axis = 0;
-    if (2 * j >= a.dim[0]) {
-        j -= a.dim[0] / 2;
-        axis = 1;
-        if (2 * j >= a.dim[1]) {
-            j -= a.dim[1] / 2;
-            axis = 2;
-        }
+// Axis of pair j, and its number in the axis' section.
+__device__ __forceinline__ int axis_of(const RotaryArgs &a, int &j) {
+    if (2 * j < a.dim[0]) return 0;
+    j -= a.dim[0] / 2;
+    if (2 * j < a.dim[1]) return 1;
+    j -= a.dim[1] / 2;
+    return 2;
+}
+
+// Turns of pair j per unit of position.
+__device__ __forceinline__ double frequency(const RotaryArgs &a, int j) {
+    const int axis = axis_of(a, j);
+    return exp2(-2.0 * j / a.dim[axis] * a.log2_theta) * 0.15915494309189533577;  // 1 / 2 pi
+}
+
+// Position of token t of batch element b on an axis: a 32-bit number.
+__device__ __forceinline__ int position(const RotaryArgs &a, unsigned b, long long t, int axis) {
+    if (a.positions) return a.positions[b * a.pos_bs + 3 * t + axis];
+    const long long n = a.first_token + t, area = (long long)a.height * a.width;
+    if (((n | area) >> 32) == 0) {  // a 64-bit division is some hundred instructions
+        const unsigned m = (unsigned)n;
+        return axis == 0 ? m / (unsigned)area : axis == 1 ? m / (unsigned)a.width % (unsigned)a.height : m % (unsigned)a.width;
     }
-    long long pos;
-    if (a.positions) {
-        pos = a.positions[b * a.pos_bs + 3 * t + axis];
-    } else {
-        const long long n = a.first_token + t, area = (long long)a.height * a.width;
-        if (((n | area) >> 32) == 0) {  // a 64-bit division is some hundred instructions
-            const unsigned m = (unsigned)n;
-            pos = axis == 0 ? m / (unsigned)area : axis == 1 ? m / (unsigned)a.width % (unsigned)a.height : m % (unsigned)a.width;
-        } else {
-            pos = axis == 0 ? n / area : axis == 1 ? n / a.width % a.height : n % a.width;
-        }
-    }
-    const double turns = (double)pos * (exp2(-2.0 * j / a.dim[axis] * a.log2_theta) * 0.15915494309189533577);  // 1 / 2 pi
-    return (float)(turns - rint(turns));
+    return (int)(axis == 0 ? n / area : axis == 1 ? n / a.width % a.height : n % a.width);
 }
 
 __device__ __forceinline__ float2 turn(float2 x, float2 cs) {
     return make_float2(x.x * cs.x - x.y * cs.y, x.x * cs.y + x.y * cs.x);
 }
 
-// W neighbouring elements from element i on (i a multiple of W; a row starts at 16 bytes).
+// W neighbouring elements from element i on (i a multiple of W; a row starts at 16 bytes):
+// eight of any type, or at least 8 bytes.
 template <int IO, int W>
 __device__ __forceinline__ void load_part(const void *row, size_t i, float (&f)[W]) {
     if constexpr (W == 8) {
         Vec<IO> x;
         x.load(row, i / 8);
         x.get(f);
-    } else if constexpr (W == 1) {
-        f[0] = load1<IO>(row, i);
     } else if constexpr (IO == IO_F32) {
         typedef float part __attribute__((ext_vector_type(W)));
         const part x = *reinterpret_cast<const part *>(static_cast<const float *>(row) + i);
 #pragma unroll
         for (int k = 0; k < W; ++k) f[k] = x[k];
-    } else if constexpr (IO == IO_BF16) {
-        typedef uint16_t part __attribute__((ext_vector_type(W)));
-        const part x = *reinterpret_cast<const part *>(static_cast<const uint16_t *>(row) + i);
-#pragma unroll
-        for (int k = 0; k < W; ++k) f[k] = __uint_as_float((uint32_t)x[k] << 16);
     } else {
-        float g[4];
-        uint32_t x = 0;
-        __builtin_memcpy(&x, static_cast<const char *>(row) + i, W);
-        fp8x4_to_f32(x, g);
-#pragma unroll
-        for (int k = 0; k < W; ++k) f[k] = g[k];
+        static_assert(IO == IO_BF16 && W == 4, "half a vector");
+        const uint2 x = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(row) + i);
+        f[0] = bf16_lo(x.x);
+        f[1] = bf16_hi(x.x);
+        f[2] = bf16_lo(x.y);
+        f[3] = bf16_hi(x.y);
     }
 }
 template <int IO, int W>
 __device__ __forceinline__ void store_part(void *row, size_t i, const float (&f)[W]) {
     if constexpr (W == 8) {
         OutVec<IO>::store(row, i / 8, f);
-    } else if constexpr (W == 1) {
-        store1<IO>(row, i, f[0]);
     } else if constexpr (IO == IO_F32) {
         typedef float part __attribute__((ext_vector_type(W)));
         part x;
@@ -91,80 +89,137 @@ __device__ __forceinline__ void store_part(void *row, size_t i, const float (&f)
         for (int k = 0; k < W; ++k) x[k] = f[k];
         *reinterpret_cast<part *>(static_cast<float *>(row) + i) = x;
     } else {
-        typedef uint32_t part __attribute__((ext_vector_type(W / 2)));
-        part x;
-#pragma unroll
-        for (int k = 0; k < W / 2; ++k) x[k] = pack_bf16x2(f[2 * k], f[2 * k + 1]);
-        *reinterpret_cast<part *>(static_cast<uint16_t *>(row) + i) = x;
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(row) + i) =
+            make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
     }
 }
 
-// W = 0: pairs (2i, 2i + 1); else halves, W elements at a time.
+// What a block does with its tokens: pairs (2i, 2i + 1), halves by W > 0 elements, or halves
+// through LDS.
+constexpr int NEIGHBOURS = 0, STAGED = -1;
+constexpr int STAGE_BYTES = 16 * 1024;  // of staged elements, in their own type
+
 template <int IO, int W, int TOK>
 __global__ __launch_bounds__(THREADS) void rotary_kernel(RotaryArgs a) {
+    __shared__ double freq[ROTARY_MAX_PAIRS];
     __shared__ float2 cs[TOK][ROTARY_MAX_PAIRS];
+    __shared__ int pos[TOK][3];
+    __shared__ const void *from[TOK];  // x and out of the tokens
+    __shared__ void *to[TOK];
+    __shared__ __align__(16) char stage[W == STAGED ? STAGE_BYTES : 16];
     const unsigned rows = (unsigned)(a.B * a.T), T = (unsigned)a.T;
     const float sign = a.inverse ? -1.0f : 1.0f;
+    for (int j = threadIdx.x; j < a.pairs; j += THREADS) freq[j] = frequency(a, j);
+    __syncthreads();
     for (unsigned row0 = blockIdx.x * TOK; row0 < rows; row0 += gridDim.x * TOK) {
-        const int tokens = rows - row0 < TOK ? rows - row0 : TOK;
-        for (int e = threadIdx.x; e < tokens * a.pairs; e += THREADS) {
-            const int k = TOK == 1 ? 0 : e / a.pairs, j = e - k * a.pairs;
+        const unsigned tokens = rows - row0 < TOK ? rows - row0 : TOK;
+        if (threadIdx.x < 4 * tokens) {
+            const unsigned k = threadIdx.x / 4, what = threadIdx.x % 4, b = (row0 + k) / T, t = (row0 + k) % T;
+            if (what < 3) {
+                pos[k][what] = position(a, b, t, what);
+            } else {
+                from[k] = at<IO>(a.x, (size_t)b * a.x_bs + (size_t)t * a.x_ts);
+                to[k] = at<OutIo<IO>>(a.out, (size_t)b * a.out_bs + (size_t)t * a.out_ts);
+            }
+        }
+        __syncthreads();
+        for (unsigned e = threadIdx.x; e < tokens * a.pairs; e += THREADS) {
+            const unsigned k = TOK == 1 ? 0 : e / a.pairs, j = e - k * a.pairs;
+            int i = j;
+            const double turns = (double)pos[k][axis_of(a, i)] * freq[j];
             float s, c;
-            sincospif(2.0f * part_turn(a, (row0 + k) / T, (row0 + k) % T, j), &s, &c);
+            sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
             cs[k][j] = make_float2(c, sign * s);
         }
         __syncthreads();
-        for (int k = 0; k < tokens; ++k) {
-            const unsigned b = (row0 + k) / T, t = (row0 + k) % T;
-            const void *px = at<IO>(a.x, (size_t)b * a.x_bs + (size_t)t * a.x_ts);
-            void *po = at<OutIo<IO>>(a.out, (size_t)b * a.out_bs + (size_t)t * a.out_ts);
-            if constexpr (W == 0) {
-                const int V = a.d / 8;
-                for (int e = threadIdx.x; e < a.H * V; e += THREADS) {
-                    Vec<IO> x;
-                    float f[8];
-                    x.load(px, e);
-                    x.get(f);
-                    const int j0 = e % V * 4;
+        if constexpr (W == NEIGHBOURS) {
+            // vector v of token k, number c of its head; divisions only before the loop
+            const unsigned V = a.d / 8, HV = a.H * V, step = THREADS % V;
+            unsigned k = TOK == 1 ? 0 : threadIdx.x / HV, v = threadIdx.x - k * HV, c = threadIdx.x % V;
+            if (TOK == 1 && v >= HV) k = 1;
+            while (k < tokens) {
+                Vec<IO> x;
+                float f[8];
+                x.load(from[k], v);
+                x.get(f);
+                const int j0 = c * 4;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (j0 + i < a.pairs) {
-                            const float2 y = turn(make_float2(f[2 * i], f[2 * i + 1]), cs[k][j0 + i]);
-                            f[2 * i] = y.x;
-                            f[2 * i + 1] = y.y;
-                        }
-                    OutVec<IO>::store(po, e, f);
-                }
-            } else {
-                // a head's parts: its pairs, W at a time, then what passes through
-                const int P = a.pairs / W, per = P + (a.d - 2 * a.pairs) / W;
-                for (int e = threadIdx.x; e < a.H * per; e += THREADS) {
-                    const int h = e / per, p = e - h * per, j = p * W;
-                    const size_t head = (size_t)h * a.d;
-                    float f[W];
-                    if (p < P) {
-                        // section starts 2 `before` into the head, pair j is its number j - before
-                        const int d0 = a.dim[0] / 2, d1 = a.dim[1] / 2;
-                        const int before = j < d0 ? 0 : j < d0 + d1 ? d0 : d0 + d1;
-                        const int half = j < d0 ? d0 : j < d0 + d1 ? d1 : a.dim[2] / 2;
-                        const size_t i0 = head + before + j, i1 = i0 + half;
-                        float g[W];
-                        load_part<IO, W>(px, i0, f);
-                        load_part<IO, W>(px, i1, g);
-#pragma unroll
-                        for (int i = 0; i < W; ++i) {
-                            const float2 z = turn(make_float2(f[i], g[i]), cs[k][j + i]);
-                            f[i] = z.x;
-                            g[i] = z.y;
-                        }
-                        store_part<IO, W>(po, i0, f);
-                        store_part<IO, W>(po, i1, g);
-                    } else {
-                        const size_t i = head + 2 * a.pairs + (p - P) * W;
-                        load_part<IO, W>(px, i, f);
-                        store_part<IO, W>(po, i, f);
+                for (int i = 0; i < 4; ++i)
+                    if (j0 + i < a.pairs) {
+                        const float2 y = turn(make_float2(f[2 * i], f[2 * i + 1]), cs[k][j0 + i]);
+                        f[2 * i] = y.x;
+                        f[2 * i + 1] = y.y;
                     }
+                OutVec<IO>::store(to[k], v, f);
+                for (v += THREADS; v >= HV && k < tokens; v -= HV) ++k;
+                c += step;
+                if (c >= V) c -= V;
+            }
+        } else if constexpr (W > 0) {
+            // a head's parts: its pairs, W at a time, then what passes through
+            const unsigned P = a.pairs / W, per = P + (a.d - 2 * a.pairs) / W, HP = a.H * per;
+            const int d0 = a.dim[0] / 2, d1 = a.dim[1] / 2;
+            for (unsigned e = threadIdx.x; e < tokens * HP; e += THREADS) {
+                const unsigned k = TOK == 1 ? 0 : e / HP, hp = e - k * HP, h = hp / per, p = hp - h * per;
+                const int j = p * W;
+                const size_t head = (size_t)h * a.d;
+                float f[W];
+                if (p < P) {
+                    // section starts 2 `before` into the head, pair j is its number j - before
+                    const int before = j < d0 ? 0 : j < d0 + d1 ? d0 : d0 + d1;
+                    const int half = j < d0 ? d0 : j < d0 + d1 ? d1 : a.dim[2] / 2;
+                    const size_t i0 = head + before + j, i1 = i0 + half;
+                    float g[W];
+                    load_part<IO, W>(from[k], i0, f);
+                    load_part<IO, W>(from[k], i1, g);
+#pragma unroll
+                    for (int i = 0; i < W; ++i) {
+                        const float2 z = turn(make_float2(f[i], g[i]), cs[k][j + i]);
+                        f[i] = z.x;
+                        g[i] = z.y;
+                    }
+                    store_part<IO, W>(to[k], i0, f);
+                    store_part<IO, W>(to[k], i1, g);
+                } else {
+                    const size_t i = head + 2 * a.pairs + (p - P) * W;
+                    load_part<IO, W>(from[k], i, f);
+                    store_part<IO, W>(to[k], i, f);
                 }
+            }
+        } else {
+            // (token, head) number u of the block's tokens x H, as many at a time as fit in LDS
+            const unsigned V = a.d / 8, units = tokens * a.H, fit = STAGE_BYTES / (a.d * io_in_bytes(IO));
+            const int d0 = a.dim[0] / 2, d1 = a.dim[1] / 2, d2 = a.dim[2] / 2;
+            for (unsigned u0 = 0; u0 < units; u0 += fit) {
+                const unsigned n = units - u0 < fit ? units - u0 : fit;
+                for (unsigned e = threadIdx.x; e < n * V; e += THREADS) {
+                    const unsigned u = e / V, k = TOK == 1 ? 0 : (u0 + u) / a.H, h = u0 + u - k * a.H;
+                    Vec<IO> x;
+                    x.load(from[k], h * V + (e - u * V));
+                    reinterpret_cast<Vec<IO> *>(stage)[e] = x;
+                }
+                __syncthreads();
+                for (unsigned e = threadIdx.x; e < n * V; e += THREADS) {
+                    const unsigned u = e / V, k = TOK == 1 ? 0 : (u0 + u) / a.H, h = u0 + u - k * a.H, v = e - u * V;
+                    float f[8];
+                    reinterpret_cast<const Vec<IO> *>(stage)[e].get(f);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        // element c of the head: pair before + (place in its half)
+                        const int c = v * 8 + i;
+                        if (c < 2 * a.pairs) {
+                            const int before = c < 2 * d0 ? 0 : c < 2 * (d0 + d1) ? d0 : d0 + d1;
+                            const int half = c < 2 * d0 ? d0 : c < 2 * (d0 + d1) ? d1 : d2;
+                            const int in = c - 2 * before;
+                            const bool second = in >= half;
+                            const float other = load1<IO>(stage, (size_t)u * a.d + c + (second ? -half : half));
+                            const float2 w = cs[k][before + in - (second ? half : 0)];
+                            f[i] = second ? other * w.y + f[i] * w.x : f[i] * w.x - other * w.y;
+                        }
+                    }
+                    OutVec<IO>::store(to[k], h * V + v, f);
+                }
+                __syncthreads();
             }
         }
         __syncthreads();  // the angles are read above and written for the next tokens
@@ -177,7 +232,7 @@ hipError_t launch(const RotaryArgs &a, hipStream_t s) {
     // would leave CUs idle (rows below 4 blocks of 4 tokens a CU).
     const long long rows = a.B * a.T;
     if (rows >= 4096)
-        rotary_kernel<IO, W, 4><<<dim3((unsigned)std::min<long long>((rows + 3) / 4, 1 << 20)), dim3(THREADS), 0, s>>>(a);
+        rotary_kernel<IO, W, 4><<<dim3((unsigned)std::min<long long>((rows + 3) / 4, ROTARY_BLOCKS)), dim3(THREADS), 0, s>>>(a);
     else
         rotary_kernel<IO, W, 1><<<dim3((unsigned)rows), dim3(THREADS), 0, s>>>(a);
     return hipGetLastError();
@@ -185,10 +240,14 @@ hipError_t launch(const RotaryArgs &a, hipStream_t s) {
 
 template <int IO>
 hipError_t launch(const RotaryArgs &a, hipStream_t s) {
-    if (!a.halves) return launch<IO, 0>(a, s);
+    if (!a.halves) return launch<IO, NEIGHBOURS>(a, s);
     const int all = a.dim[0] / 2 | a.dim[1] / 2 | a.dim[2] / 2;
-    return all % 8 == 0 ? launch<IO, 8>(a, s) : all % 4 == 0 ? launch<IO, 4>(a, s) : all % 2 == 0 ? launch<IO, 2>(a, s)
-                                                                                        : launch<IO, 1>(a, s);
+    if (all % 8 == 0) return launch<IO, 8>(a, s);
+    if constexpr (IO != IO_FP8)
+        if (all % 4 == 0) return launch<IO, 4>(a, s);
+    if constexpr (IO == IO_F32)
+        if (all % 2 == 0) return launch<IO, 2>(a, s);
+    return launch<IO, STAGED>(a, s);
 }
 
 }  // namespace
