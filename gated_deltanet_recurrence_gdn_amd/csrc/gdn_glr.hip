@@ -18,6 +18,13 @@
 //    have drawn; the smallest of them waits for nobody.
 //  * A published word is 64 bits, value and the call's number, read and written by single
 //    relaxed atomics at device scope: nothing else has to be ordered around it.
+//  * A block that waits asks for one channel's words: whole rows of words in every round would
+//    fill the fabric that the tokens come through.
+//  * Two waves look back, 64 channels each, four maps at a time.  Where a call has few slabs its
+//    time is that of the chain (all its tiles run at once): there all eight waves take 16
+//    channels each and sixteen maps at a time, up to 64 tiles back (2 x 33,563 tokens of 128
+//    channels: 39 us against 66; but 141 us against 150 the other way round at 20 slabs, where
+//    the barrier that it needs costs more than the wait).
 //  * The block that draws a slab's last number sets the counter to the next call's number
 //    and 0, so a call leaves the workspace ready for the next one (or for its own
 //    replay in a graph) without a clearing pass.  The call's number has 32 bits.
@@ -31,7 +38,8 @@ namespace {
 
 constexpr int LANES = 64, SLAB = 2 * LANES;  // channels of a block
 constexpr int WAVES = 8;
-constexpr int LOOK = 16;                     // how far back a tile looks at once
+constexpr int LOOK = 16;                     // how far back a wave looks at once
+constexpr int OWN = SLAB / WAVES, FEW = 8;   // channels of a wave of eight that look back; up to FEW slabs
 
 // Tokens of a wave.  The chain costs a tile some microseconds whatever its size, so tiles are
 // as long as their inputs fit in registers with two blocks on a CU (128 registers a lane).
@@ -65,6 +73,7 @@ __device__ __forceinline__ bool known(u64 w, uint32_t call) {  // in every lane 
 // look back hold their tokens in registers meanwhile.
 struct Window {
     float m[LOOK][SLAB], d[LOOK][SLAB];
+    int back;
 };
 
 // State before tile k > 0 of channel i of the slab; one whole wave.  `at` and `mat` are its
@@ -112,6 +121,69 @@ __device__ float state_before(const Chain &c, Window &win, int i, uint32_t call,
         }
         __builtin_amdgcn_s_sleep(1);
     }
+}
+
+// State before tile k > 0 of channel `c` of the slab; the whole block, lanes l, l + 16, l + 32
+// and l + 48 of wave w for channel 16 w + l.  `base` is the slab's first word of tile k;
+// `share` channels have one word in the plane mul.  (A, H) is the tile's own map.
+__device__ float state_before_by_block(const Chain &ch, Window &win, uint32_t call, int k, size_t base, int share, float A,
+                                       float H) {
+    const size_t step = (size_t)ch.slabs * SLAB;
+    const int lane = threadIdx.x % LANES, wave = threadIdx.x / LANES, c = wave * OWN + lane % OWN, q = lane / OWN;
+    const size_t at = base + c, mat = at - c % share;
+    if (q == 0) {
+        post(ch.add + at, word(call, H));
+        if (c % share == 0) post(ch.mul + mat, word(call, A));
+    }
+    if (wave == 0) {
+        // lane l: the tile l + 1 back; the nearest known end state with known maps behind it
+        const int far = k < LANES ? k : LANES;
+        const size_t there = base - step * (lane < far ? lane + 1 : far);
+        int j;
+        for (;;) {
+            const u64 e = peek(ch.end + there), d = peek(ch.add + there);
+            const u64 ends = __ballot(lane < far && (uint32_t)(e >> 32) == call);
+            const u64 maps = __ballot((uint32_t)(d >> 32) == call);
+            j = __ffsll(ends);
+            const u64 behind = j ? ((u64)1 << (j - 1)) - 1 : 0;
+            if (j && (maps & behind) == behind) break;
+            __builtin_amdgcn_s_sleep(1);
+        }
+        if (lane == 0) win.back = j;
+    }
+    __syncthreads();
+    // These words are there or on their way: the blocks that post them do not wait for this one.
+    const int j = win.back;
+    u64 e;
+    do e = peek(ch.end + at - step * j);
+    while (!known(e, call));
+    float s = value(e);
+#pragma unroll 1
+    for (int hi = j - 1; hi >= 1; hi -= 16) {
+        u64 wm[4], wd[4];
+        bool ok;
+        do {
+            ok = true;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int o = hi - 4 * u - q;
+                const size_t back = step * (o >= 1 ? o : 1);
+                wm[u] = peek(ch.mul + mat - back);
+                wd[u] = peek(ch.add + at - back);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) ok = ok && known(wm[u], call) && known(wd[u], call);
+        } while (!ok);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            win.m[4 * u + q][c] = value(wm[u]);
+            win.d[4 * u + q][c] = value(wd[u]);
+        }
+        const int n = hi < 16 ? hi : 16;
+#pragma unroll 1
+        for (int t = 0; t < n; ++t) s = fmaf(win.m[t][c], s, win.d[t][c]);
+    }
+    return s;
 }
 
 // Two neighbouring elements, as they lie in memory: elements c and c + 1 of a row.
@@ -279,7 +351,7 @@ __device__ __forceinline__ void load_pairs(P (&v)[R], const void *base, int C, c
             if (r >= p.n) v[r].zero();
 }
 
-template <int IO, bool CH, bool BETA, int R>
+template <int IO, bool CH, bool BETA, int R, bool FEWS>
 __global__ __launch_bounds__(WAVES * LANES, 4) void glr_forward_kernel(GlrArgs a, Chain chain) {
     __shared__ float sA[WAVES][SLAB], sH[WAVES][SLAB], sC[SLAB];
     __shared__ float sGa[Gates<CH, R>::STAGE], sGb[BETA ? Gates<CH, R>::STAGE : 1];
@@ -321,9 +393,10 @@ __global__ __launch_bounds__(WAVES * LANES, 4) void glr_forward_kernel(GlrArgs a
     lds2(sA[wave], lane) = A;
     lds2(sH[wave], lane) = H;
     __syncthreads();
-    // the tile's map and start state, a channel per thread
+    // the tile's map and start state: a channel per thread of the first two waves, or all waves
+    // for 16 channels each
     const int share = CH ? 1 : a.d;  // channels with one decay
-    for (int i = threadIdx.x; i < SLAB; i += blockDim.x) {
+    for (int i = FEWS ? wave * OWN + lane % OWN : threadIdx.x; i < SLAB; i += FEWS ? SLAB : blockDim.x) {
         float tA = sA[0][i], tH = sH[0][i], s = 0.0f;
         for (int w = 1; w < waves; ++w) {
             tH = fmaf(sA[w][i], tH, sH[w][i]);
@@ -331,11 +404,15 @@ __global__ __launch_bounds__(WAVES * LANES, 4) void glr_forward_kernel(GlrArgs a
         }
         const int ch = p.slab_c0 + i;
         const size_t st = (size_t)p.b * C + ch, wd = ((size_t)at.tile * chain.slabs + at.slab) * SLAB + i;
-        if (at.tile > 0)
-            s = state_before(chain, window, i, at.call, at.tile, wd, wd - i % share, i % share == 0, tA, tH);
-        else if (a.state_in && ch < C)
+        if (at.tile > 0) {
+            if constexpr (FEWS)
+                s = state_before_by_block(chain, window, at.call, at.tile, wd - i, share, tA, tH);
+            else
+                s = state_before(chain, window, i, at.call, at.tile, wd, wd - i % share, i % share == 0, tA, tH);
+        } else if (a.state_in && ch < C)
             s = a.state_in[st];
         const float e = fmaf(tA, s, tH);
+        if (FEWS && lane >= OWN) continue;  // these lanes repeat the first ones' channels
         if (at.tile + 1 < chain.tiles)
             post(chain.end + wd, word(at.call, e));
         else if (a.state_out && ch < C)
@@ -406,7 +483,7 @@ __device__ __forceinline__ void group_sums(float (&v)[N], int L, int lane) {
     if (L >= 64) v[0] += __shfl_xor(v[0], 32);
 }
 
-template <int IO, bool CH, bool BETA, int R>
+template <int IO, bool CH, bool BETA, int R, bool FEWS>
 __global__ __launch_bounds__(WAVES * LANES, 4) void glr_backward_kernel(GlrArgs a, Chain chain) {
     static_assert(WAVES * R % GLR_TILE == 0 && GLR_TILE % R == 0 && R % 8 == 0, "a tile starts at a saved state");
     __shared__ float sA[WAVES][SLAB], sH[WAVES][SLAB], sG[WAVES][SLAB], sC[SLAB];
@@ -459,7 +536,7 @@ __global__ __launch_bounds__(WAVES * LANES, 4) void glr_backward_kernel(GlrArgs 
     lds2(sG[wave], lane) = G;
     __syncthreads();
     const int share = CH ? 1 : a.d;
-    for (int i = threadIdx.x; i < SLAB; i += blockDim.x) {
+    for (int i = FEWS ? wave * OWN + lane % OWN : threadIdx.x; i < SLAB; i += FEWS ? SLAB : blockDim.x) {
         float tA = 1.0f, tG = 0.0f, in = 0.0f;
         for (int w = waves - 1; w >= 0; --w) {
             tG = fmaf(sA[w][i], tG, sG[w][i]);
@@ -467,11 +544,15 @@ __global__ __launch_bounds__(WAVES * LANES, 4) void glr_backward_kernel(GlrArgs 
         }
         const int ch = p.slab_c0 + i;
         const size_t st = (size_t)p.b * C + ch, wd = ((size_t)at.tile * chain.slabs + at.slab) * SLAB + i;
-        if (at.tile > 0)
-            in = state_before(chain, window, i, at.call, at.tile, wd, wd - i % share, i % share == 0, tA, tG);
-        else if (a.dstate_out && ch < C)
+        if (at.tile > 0) {
+            if constexpr (FEWS)
+                in = state_before_by_block(chain, window, at.call, at.tile, wd - i, share, tA, tG);
+            else
+                in = state_before(chain, window, i, at.call, at.tile, wd, wd - i % share, i % share == 0, tA, tG);
+        } else if (a.dstate_out && ch < C)
             in = a.dstate_out[st];
         const float e = fmaf(tA, in, tG);
+        if (FEWS && lane >= OWN) continue;
         if (tile > 0)
             post(chain.end + wd, word(at.call, e));
         else if (a.dstate_in && ch < C)
@@ -577,10 +658,13 @@ bool fills(const GlrArgs &a, int R) {
     return a.T >= WAVES * R && slabs_of(a.B, a.H, a.d) * ((a.T + WAVES * R - 1) / (WAVES * R)) >= 2LL * a.ncu;
 }
 
-template <int IO, bool CH, bool BETA, int R>
+bool few_slabs(const GlrArgs &a, int R) { return slabs_of(a.B, a.H, a.d) <= FEW && a.T > WAVES * R; }
+
+template <int IO, bool CH, bool BETA, int R, bool FEWS = false>
 hipError_t forward_by(const GlrArgs &a, hipStream_t s) {
     const Chain c = chain_of(a, WAVES * R);
-    glr_forward_kernel<IO, CH, BETA, R><<<dim3((unsigned)(c.slabs * c.tiles)), dim3(waves_of(a, R) * LANES), 0, s>>>(a, c);
+    glr_forward_kernel<IO, CH, BETA, R, FEWS>
+        <<<dim3((unsigned)(c.slabs * c.tiles)), dim3(waves_of(a, R) * LANES), 0, s>>>(a, c);
     return hipGetLastError();
 }
 template <int IO, bool CH, bool BETA>
@@ -590,19 +674,22 @@ hipError_t forward(const GlrArgs &a, hipStream_t s) {
         glr_step_kernel<IO, CH, BETA><<<dim3((unsigned)((lanes + 255) / 256)), dim3(256), 0, s>>>(a);
         return hipGetLastError();
     }
+    if (few_slabs(a, 16)) return forward_by<IO, CH, BETA, 16, true>(a, s);
     constexpr int R = fwd_tokens(IO, CH);
     if constexpr (R > 16)
         if (fills(a, R)) return forward_by<IO, CH, BETA, R>(a, s);
     return forward_by<IO, CH, BETA, 16>(a, s);
 }
-template <int IO, bool CH, bool BETA, int R>
+template <int IO, bool CH, bool BETA, int R, bool FEWS = false>
 hipError_t backward_by(const GlrArgs &a, hipStream_t s) {
     const Chain c = chain_of(a, WAVES * R);
-    glr_backward_kernel<IO, CH, BETA, R><<<dim3((unsigned)(c.slabs * c.tiles)), dim3(waves_of(a, R) * LANES), 0, s>>>(a, c);
+    glr_backward_kernel<IO, CH, BETA, R, FEWS>
+        <<<dim3((unsigned)(c.slabs * c.tiles)), dim3(waves_of(a, R) * LANES), 0, s>>>(a, c);
     return hipGetLastError();
 }
 template <int IO, bool CH, bool BETA>
 hipError_t backward(const GlrArgs &a, hipStream_t s) {
+    if (few_slabs(a, 8)) return backward_by<IO, CH, BETA, 8, true>(a, s);
     constexpr int R = bwd_tokens(IO, CH);
     if constexpr (R > 8)
         if (fills(a, R)) return backward_by<IO, CH, BETA, R>(a, s);
