@@ -5,8 +5,9 @@
 // eight neighbouring channels (a 16-byte vector in bf16) and a fixed place in the row, so that
 // weight and bias stay in registers; V = C / 8 threads make a row, and a block has
 // R = threads / V rows at once.  Three forms by the size of a sample:
-//  * rows (S = 1, D = C / G channels of a group, D / 8 a power of two up to 64): a group is
-//    D / 8 lanes of a wave; its sums are exchanges between lanes and the row is read once.
+//  * rows (S = 1, D = C / G channels of a group a multiple of 8 up to 512): a group is D / 8
+//    lanes of a wave, or the power of two above with the rest idle; its sums are exchanges
+//    between lanes and the row is read once.
 //  * resident (small samples): a block has a sample, in registers for the forward pass, and
 //    joins its groups through LDS; one launch.
 //  * split (larger samples): a sample is cut into stretches of rows.  One launch forms each
@@ -27,6 +28,7 @@ namespace {
 constexpr int RES_K = 4;        // rows of a thread in the resident form
 constexpr int ROWS_U = 4;       // rows a thread of the other forms has in flight
 constexpr int BATCH = 1024;     // samples of one round of the split form (bounds the workspace)
+constexpr int JOIN_HERE = 2048; // stretches times groups of a sample that each block may join for itself
 
 // 1 / (1 + e^-z) with the hardware's exponential and reciprocal (an ulp each; the IEEE
 // forms would make the pass bound by the vector units).
@@ -71,10 +73,23 @@ __device__ __forceinline__ float inv_std(float var, float eps) { return __builti
 
 // ---- rows ---------------------------------------------------------------------------
 
+// A thread's place: group by group, L lanes each (P = V / G of them used), a row after another.
+struct Place {
+    int row, col;
+    bool on;  // idle lanes repeat the first vector of their group
+    __device__ __forceinline__ Place(const GroupNormArgs &a, int V, int R, int L) {
+        const int P = V / a.G, width = a.G * L, at = threadIdx.x % width, i = at % L;
+        row = threadIdx.x / width;
+        col = at / L * P + (i < P ? i : 0);
+        on = row < R && i < P;
+    }
+};
+
 template <int IO, bool SILU>
-__global__ __launch_bounds__(512) void rows_forward_kernel(GroupNormArgs a, int V, int R) {
-    const int row = threadIdx.x / V, col = threadIdx.x % V, P = a.C / a.G / 8;
-    const bool on = row < R;
+__global__ __launch_bounds__(512) void rows_forward_kernel(GroupNormArgs a, int V, int R, int L) {
+    const Place p(a, V, R, L);
+    const int row = p.row, col = p.col, P = V / a.G;
+    const bool on = p.on;
     float w[8], b[8];
     channel8(w, a.weight, col, 1.0f);
     channel8(b, a.bias, col, 0.0f);
@@ -85,7 +100,7 @@ __global__ __launch_bounds__(512) void rows_forward_kernel(GroupNormArgs a, int 
 #pragma unroll
         for (int u = 0; u < ROWS_U; ++u) {
             const long long n = n0 + u * step + row;
-            if (on && n < a.N) x[u].load(a.x, (size_t)n * V + col);
+            if (row < R && n < a.N) x[u].load(a.x, (size_t)n * V + col);
         }
 #pragma unroll
         for (int u = 0; u < ROWS_U; ++u) {
@@ -94,13 +109,13 @@ __global__ __launch_bounds__(512) void rows_forward_kernel(GroupNormArgs a, int 
             x[u].get(f);
 #pragma unroll
             for (int i = 0; i < 8; ++i) s += f[i];
-            const float mean = lanes_sum(s, P) * inv;
+            const float mean = lanes_sum(on ? s : 0.0f, L) * inv;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 f[i] -= mean;
                 q = fmaf(f[i], f[i], q);
             }
-            const float rstd = inv_std(lanes_sum(q, P) * inv, a.eps);
+            const float rstd = inv_std(lanes_sum(on ? q : 0.0f, L) * inv, a.eps);
 #pragma unroll
             for (int i = 0; i < 8; ++i) f[i] = act<SILU>(fmaf(f[i] * rstd, w[i], b[i]));
             if (on && n < a.N) {
@@ -134,10 +149,11 @@ __device__ __forceinline__ void block_channels(const float (&s1)[8], const float
 }
 
 template <int IO, bool SILU>
-__global__ __launch_bounds__(512) void rows_backward_kernel(GroupNormArgs a, int V, int R, float *part) {
+__global__ __launch_bounds__(512) void rows_backward_kernel(GroupNormArgs a, int V, int R, int L, float *part) {
     extern __shared__ float lds[];
-    const int row = threadIdx.x / V, col = threadIdx.x % V, P = a.C / a.G / 8;
-    const bool on = row < R;
+    const Place p(a, V, R, L);
+    const int row = p.row, col = p.col, P = V / a.G;
+    const bool on = p.on;
     float w[8], b[8], sw[8] = {}, sb[8] = {};
     channel8(w, a.weight, col, 1.0f);
     channel8(b, a.bias, col, 0.0f);
@@ -151,7 +167,7 @@ __global__ __launch_bounds__(512) void rows_backward_kernel(GroupNormArgs a, int
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const long long n = n0 + u * step + row;
-            if (on && n < a.N) {
+            if (row < R && n < a.N) {
                 x[u].load(a.x, (size_t)n * V + col);
                 y[u].load(a.dout, (size_t)n * V + col);
                 st[u] = reinterpret_cast<const float2 *>(a.stats)[(size_t)n * a.G + col / P];
@@ -176,13 +192,13 @@ __global__ __launch_bounds__(512) void rows_backward_kernel(GroupNormArgs a, int
                 s1 += t[i];
                 s2 = fmaf(t[i], f[i], s2);
             }
-            const float m1 = lanes_sum(s1, P) * inv, m2 = lanes_sum(s2, P) * inv;
+            const float m1 = lanes_sum(on ? s1 : 0.0f, L) * inv, m2 = lanes_sum(on ? s2 : 0.0f, L) * inv;
 #pragma unroll
             for (int i = 0; i < 8; ++i) t[i] = st[u].y * (t[i] - m1 - f[i] * m2);
             if (in && a.dx) OutVec<IO>::store(a.dx, (size_t)n * V + col, t);
         }
     }
-    if (part) block_channels(sb, sw, lds, part, a.C, row, col, R);
+    if (part) block_channels(sb, sw, lds, part, a.C, on ? row : R, col, R);
 }
 
 // ---- joining a block's threads by group ---------------------------------------------
@@ -563,20 +579,48 @@ __global__ __launch_bounds__(256) void split_stats_join_kernel(GroupNormArgs a, 
     if (threadIdx.x == 0) stats[(size_t)n * a.G + g] = make_float2(mean, inv_std(q / total, a.eps));
 }
 
+// `part`: the stretches are joined here (few of them: each block does so for its sample), the
+// first block of a sample writing stats_out; else stats holds the results.
 template <int IO, bool SILU>
 __global__ __launch_bounds__(1024) void split_apply_kernel(GroupNormArgs a, int V, int R, Split sp, long long n0,
-                                                           const float2 *stats) {
+                                                           const float2 *stats, const float2 *part) {
+    extern __shared__ float lds[];
     const int row = threadIdx.x / V, col = threadIdx.x % V, D = a.C / a.G;
-    if (row >= R) return;
     const int ny = gridDim.y - 1 - blockIdx.y;
     const long long j = sp.count - 1 - (int)blockIdx.x, n = n0 + ny;
     const long long lo = j * sp.len, hi = lo + sp.len < a.S ? lo + sp.len : a.S;
+    stats += (size_t)ny * a.G;
+    if (part) {
+        float2 *group = reinterpret_cast<float2 *>(lds);
+        const float2 *p = part + (size_t)ny * sp.count * a.G;
+        const float total = (float)a.S * (float)D, full = (float)sp.len * (float)D;
+        const float last = (float)(a.S - (sp.count - 1) * sp.len) * (float)D;
+        each_group(a.G, sp.count, [&](int g, int lane, int L) {
+            const bool in = g < a.G;
+            float s = 0.0f, q = 0.0f;
+            for (int k = lane; in && k < sp.count; k += L) s = fmaf((k + 1 < sp.count ? full : last) / total, p[k * a.G + g].x, s);
+            const float m = lanes_sum(s, L);
+            for (int k = lane; in && k < sp.count; k += L) {
+                const float2 v = p[k * a.G + g];
+                q += fmaf((k + 1 < sp.count ? full : last) * (v.x - m), v.x - m, v.y);
+            }
+            q = lanes_sum(q, L);
+            if (in && lane == 0) {
+                const float2 st = make_float2(m, inv_std(q / total, a.eps));
+                group[g] = st;
+                if (a.stats_out && blockIdx.x == 0) reinterpret_cast<float2 *>(a.stats_out)[(size_t)n * a.G + g] = st;
+            }
+        });
+        __syncthreads();
+        stats = group;
+    }
+    if (row >= R) return;
     float mean[8], scale[8], b[8];
     channel8(scale, a.weight, col, 1.0f);
     channel8(b, a.bias, col, 0.0f);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float2 st = stats[(size_t)ny * a.G + (8 * col + i) / D];
+        const float2 st = stats[(8 * col + i) / D];
         mean[i] = st.x;
         scale[i] *= st.y;
     }
@@ -740,10 +784,23 @@ Layout layout(int C, int at_least) {
     return l;
 }
 
-bool rows_form(const GroupNormArgs &a) {
+// Lanes of a group in the rows form: the power of two from D / 8 on; 0 where the form does not
+// apply.
+int rows_lanes(const GroupNormArgs &a) {
     const int D = a.C / a.G, P = D / 8;
-    return a.S == 1 && D % 8 == 0 && (P & (P - 1)) == 0 && P <= 64 && a.C / 8 <= 512;
+    if (a.S != 1 || D % 8 || P > 64) return 0;
+    int L = 1;
+    while (L < P) L *= 2;
+    return a.G * L <= 512 ? L : 0;
 }
+Layout rows_layout(const GroupNormArgs &a, int L) {
+    Layout l;
+    l.V = a.C / 8;
+    l.threads = std::max(256, (a.G * L + 63) / 64 * 64);
+    l.R = l.threads / (a.G * L);
+    return l;
+}
+
 // At most RES_K rows of a thread.  A sample that fits is faster here than split even if it is
 // alone (3 x 77 x 320 fp32, forward and backward: 27 us, split 37 us: two launches more each).
 bool resident_form(const GroupNormArgs &a) { return a.S <= RES_K * (1024 / (a.C / 8)); }
@@ -799,12 +856,12 @@ Work work_of(const GroupNormArgs &a) {
 
 template <int IO, bool SILU>
 hipError_t forward(const GroupNormArgs &a, hipStream_t s) {
-    if (rows_form(a)) {
-        const Layout l = layout(a.C, 256);
+    if (const int L = rows_lanes(a)) {
+        const Layout l = rows_layout(a, L);
         // 24 waves a CU, where 16 to 20 fit at once: 65,520 x 4096 bf16 takes 220 us, with 16
         // waves 240, with 64 or 128 waves 232 to 235
         const long long blocks = std::min<long long>((a.N + l.R - 1) / l.R, blocks_for(a.ncu, l.threads) * 3 / 2);
-        rows_forward_kernel<IO, SILU><<<dim3((unsigned)blocks), dim3(l.threads), 0, s>>>(a, l.V, l.R);
+        rows_forward_kernel<IO, SILU><<<dim3((unsigned)blocks), dim3(l.threads), 0, s>>>(a, l.V, l.R, L);
         return hipGetLastError();
     }
     if (resident_form(a)) {
@@ -825,8 +882,13 @@ hipError_t forward(const GroupNormArgs &a, hipStream_t s) {
         const dim3 grid(sp.count, samples), block(l.threads);
         float2 *stats = a.stats_out ? reinterpret_cast<float2 *>(a.stats_out) + n0 * a.G : w.group;
         split_stats_kernel<IO><<<grid, block, lds, s>>>(a, l.V, l.R, sp, n0, reinterpret_cast<float2 *>(w.part));
-        split_stats_join_kernel<<<dim3(a.G, samples), dim3(256), 0, s>>>(a, sp, reinterpret_cast<const float2 *>(w.part), stats);
-        split_apply_kernel<IO, SILU><<<grid, block, 0, s>>>(a, l.V, l.R, sp, n0, stats);
+        const float2 *part = reinterpret_cast<const float2 *>(w.part);
+        if (sp.count * a.G <= JOIN_HERE) {
+            split_apply_kernel<IO, SILU><<<grid, block, a.G * sizeof(float2), s>>>(a, l.V, l.R, sp, n0, stats, part);
+        } else {
+            split_stats_join_kernel<<<dim3(a.G, samples), dim3(256), 0, s>>>(a, sp, part, stats);
+            split_apply_kernel<IO, SILU><<<grid, block, 0, s>>>(a, l.V, l.R, sp, n0, stats, nullptr);
+        }
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
@@ -844,11 +906,11 @@ hipError_t backward(const GroupNormArgs &a, hipStream_t s) {
     const bool wanted = a.dweight || a.dbias;
     const Work w = work_of(a);
     if (a.N * a.S == 0) return wanted ? channels(a, w.part, 0, s) : hipSuccess;
-    if (rows_form(a)) {
-        const Layout l = layout(a.C, 256);
+    if (const int L = rows_lanes(a)) {
+        const Layout l = rows_layout(a, L);
         const int blocks = (int)std::min<long long>((a.N + l.R - 1) / l.R, blocks_for(a.ncu, l.threads));
         rows_backward_kernel<IO, SILU><<<dim3(blocks), dim3(l.threads), (size_t)l.R * a.C * sizeof(float), s>>>(
-            a, l.V, l.R, wanted ? w.part : nullptr);
+            a, l.V, l.R, L, wanted ? w.part : nullptr);
         return wanted ? channels(a, w.part, blocks, s) : hipGetLastError();
     }
     if (resident_form(a)) {

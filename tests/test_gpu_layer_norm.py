@@ -42,6 +42,7 @@ def parity(label, x, G, act="silu", dtype="bf16", eps=1e-5):
     (1, 2, 16, 2), (2, 77, 320, 32), (3, 9, 40, 5), (1, 1000, 8, 2), (2, 513, 64, 1), (1, 5000, 128, 32), (2, 1563, 24, 3),
     (40, 64, 512, 8), (1, 300, 8192, 16), (1, 40, 2560, 20), (7, 3, 1000, 125),
     (2, 2, 8192, 8192), (1, 70, 8192, 8192), (2, 6, 4800, 3), (1100, 1, 24, 1), (1, 300, 8, 8), (1030, 17, 1024, 64),
+    (77, 1, 80, 1), (300, 1, 24, 1), (41, 1, 1920, 12), (9, 1, 4096, 8), (130, 1, 96, 4), (20, 1, 4480, 7), (30, 700, 64, 16),
 ])
 @pytest.mark.parametrize("act", ["silu", "none"])
 def test_shapes(N, S, C, G, act):
