@@ -148,7 +148,7 @@ int rotary_check(gdn_ctx *h, const gdn_rotary_config &c, long long T, long long 
         sum += c.axis_dim[s];
     }
     if (sum > c.d) return fail(h, GDN_ERR_ARG, "the axis_dim sum to %lld, above d = %d", sum, c.d);
-    if (!(c.theta > 0.0) || !std::isfinite(c.theta)) return fail(h, GDN_ERR_ARG, "theta must be > 0 and finite");
+    if (!(c.theta >= 1.0) || !std::isfinite(c.theta)) return fail(h, GDN_ERR_ARG, "theta must be >= 1 and finite");
     if (c.flags & ~(GDN_ROTARY_HALVES | GDN_ROTARY_INVERSE)) return fail(h, GDN_ERR_ARG, "unknown flags 0x%x", c.flags);
     if (T < 0) return fail(h, GDN_ERR_ARG, "T = %lld is negative", T);
     const long long row = (long long)c.H * c.d;
@@ -214,8 +214,7 @@ gdn::GlrArgs glr_args(const gdn_ctx *h, long long T) {
 int gn_check_sizes(gdn_ctx *h, long long N, long long S) {
     if (N < 0 || S < 0) return fail(h, GDN_ERR_ARG, "N = %lld and S = %lld must be >= 0", N, S);
     if (N > h->gn.max_N) return fail(h, GDN_ERR_ARG, "N = %lld exceeds max_N = %lld", N, h->gn.max_N);
-    if (S > (1LL << 40) || (double)N * (double)S * h->gn.C > 1.0e18)
-        return fail(h, GDN_ERR_ARG, "N * S * C is too large");
+    if (S > (1LL << 30)) return fail(h, GDN_ERR_UNSUPPORTED, "S = %lld exceeds 2^30", S);
     return GDN_OK;
 }
 

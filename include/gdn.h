@@ -273,7 +273,7 @@ typedef struct {
     int d;            /* head dim, a multiple of 8, 8 .. 512                         */
     int io_dtype;     /* gdn_dtype of x                                              */
     int axis_dim[3];  /* elements turned by time, height, width: even, >= 0, sum <= d */
-    double theta;     /* base of the frequencies, > 0 and finite                     */
+    double theta;     /* base of the frequencies, >= 1 and finite                    */
     unsigned flags;   /* GDN_ROTARY_* bits                                           */
 } gdn_rotary_config;
 
@@ -390,8 +390,8 @@ typedef struct {
  * owns a workspace that its calls share (see Ownership above). */
 int gdn_group_norm_create(const gdn_group_norm_config *cfg, gdn_handle *out_h);
 
-/* stats NULL = not wanted (needed by gdn_group_norm_backward).  N = 0 or S = 0
- * writes nothing. */
+/* S at most 2^30.  stats NULL = not wanted (needed by gdn_group_norm_backward).
+ * N = 0 or S = 0 writes nothing. */
 int gdn_group_norm_forward(gdn_handle h, const void *x, const float *weight,
                            const float *bias, void *out, float *stats, long long N,
                            long long S, void *hip_stream);

@@ -155,7 +155,7 @@ def _groups(y, G):
     return y.reshape(N, S, G, C // G)
 
 
-def group_norm(x, weight, bias, G, act, eps=1e-5):
+def group_norm(x, weight, bias, G, act, eps=1e-5, sums=SUMS):
     """x [N, S, C]: (out, bound, stats, bound)."""
     x = x.double()
     g = _groups(x, G)
@@ -167,17 +167,17 @@ def group_norm(x, weight, bias, G, act, eps=1e-5):
     b = torch.zeros_like(w) if bias is None else bias.double()
     z = xhat * w + b
     out = z * torch.sigmoid(z) if act == "silu" else z
-    # the mean is off by SUMS u times the mean size, 1/std by SUMS u relative; z * sigmoid(z) has a
+    # the mean is off by `sums` u times the mean size, 1/std by `sums` u relative; z * sigmoid(z) has a
     # slope under 1.1 and its exponential and quotient are good to 16 u
-    dmean = SUMS * U * g.abs().mean((1, 3), keepdim=True)
-    dx = (dmean * rstd + SUMS * U * ((g - mean) * rstd).abs()).reshape(x.shape)
+    dmean = sums * U * g.abs().mean((1, 3), keepdim=True)
+    dx = (dmean * rstd + sums * U * ((g - mean) * rstd).abs()).reshape(x.shape)
     bound = 1.1 * (dx * w.abs() + 4 * U * (xhat * w).abs() + 4 * U * b.abs()) + 16 * U * out.abs()
     stats = torch.cat((mean, rstd), -1)[:, 0]
-    sb = torch.cat((dmean, SUMS * U * rstd * (1 + (mean * rstd) ** 2 * SUMS * U)), -1)[:, 0]
+    sb = torch.cat((dmean, sums * U * rstd * (1 + (mean * rstd) ** 2 * sums * U)), -1)[:, 0]
     return out, bound, stats, sb
 
 
-def group_norm_grad(x, weight, bias, G, act, dout, eps=1e-5):
+def group_norm_grad(x, weight, bias, G, act, dout, eps=1e-5, sums=SUMS):
     """{name: (value, bound)} of dx, dweight, dbias."""
     x, dy = x.double(), dout.double()
     N, S, C = x.shape
@@ -194,19 +194,19 @@ def group_norm_grad(x, weight, bias, G, act, dout, eps=1e-5):
     else:
         dz = dy
     # errors of xhat (as in group_norm) and, through the slope of act' (under 0.5 per unit of z), of dz
-    exhat = (SUMS * U * (g.abs().mean((1, 3), keepdim=True) * rstd + ((g - mean) * rstd).abs())).reshape(x.shape)
+    exhat = (sums * U * (g.abs().mean((1, 3), keepdim=True) * rstd + ((g - mean) * rstd).abs())).reshape(x.shape)
     edz = 16 * U * dy.abs() + (0.5 * dy.abs() * (exhat * w.abs() + 4 * U * (z.abs() + b.abs())) if act == "silu" else 0.0)
     t, et = _groups(dz * w, G), _groups(edz * w.abs() + 4 * U * (dz * w).abs(), G)
     xh, exh = _groups(xhat, G), _groups(exhat, G)
     m1, m2 = t.mean((1, 3), keepdim=True), (t * xh).mean((1, 3), keepdim=True)
     dims = dict(dim=(1, 3), keepdim=True)
-    em1 = et.mean(**dims) + SUMS * U * t.abs().mean(**dims)
-    em2 = (et * xh.abs() + t.abs() * exh).mean(**dims) + SUMS * U * (t * xh).abs().mean(**dims)
+    em1 = et.mean(**dims) + sums * U * t.abs().mean(**dims)
+    em2 = (et * xh.abs() + t.abs() * exh).mean(**dims) + sums * U * (t * xh).abs().mean(**dims)
     dx = rstd * (t - m1 - xh * m2)
-    edx = rstd * (et + em1 + xh.abs() * em2 + exh * m2.abs()) + SUMS * U * rstd * (t.abs() + m1.abs() + (xh * m2).abs())
+    edx = rstd * (et + em1 + xh.abs() * em2 + exh * m2.abs()) + sums * U * rstd * (t.abs() + m1.abs() + (xh * m2).abs())
     dw, db = (dz * xhat).sum((0, 1)), dz.sum((0, 1))
-    edw = (edz * xhat.abs() + dz.abs() * exhat).sum((0, 1)) + SUMS * U * (dz * xhat).abs().sum((0, 1))
-    edb = edz.sum((0, 1)) + SUMS * U * dz.abs().sum((0, 1))
+    edw = (edz * xhat.abs() + dz.abs() * exhat).sum((0, 1)) + sums * U * (dz * xhat).abs().sum((0, 1))
+    edb = edz.sum((0, 1)) + sums * U * dz.abs().sum((0, 1))
     return {"dx": (dx.reshape(x.shape), edx.reshape(x.shape)), "dweight": (dw, edw), "dbias": (db, edb)}
 
 

@@ -129,6 +129,37 @@ def test_captured_and_replayed():
         h.close()
 
 
+def test_two_graphs_of_one_handle():
+    """Two graphs captured from the same handles and replayed in turn share the handles' workspace."""
+    B, T, H, d = 1, 1500, 2, 64
+    xs = [lo.cuda(lo.glr_inputs(62 + i, B, T, H, d, "head")) for i in range(2)]
+    frames = [lo.randn(lo.gen(64 + i), 1, 6000, 64, dtype="bf16").cuda() for i in range(2)]
+    w, ones = torch.ones((H * d,), device="cuda"), torch.ones((64,), device="cuda")
+    r, n, m = gb.GLR(B, H, d, max_T=T), gb.GroupNorm(H * d, H, max_N=B * T), gb.GroupNorm(64, 8, max_N=1)
+
+    def step(i):
+        fo, fs = m.forward(frames[i], ones, ones)
+        return (*train_step(r, n, xs[i], w, w), fo, *m.backward(frames[i], ones, ones, fs, frames[i]))
+
+    eager = [[y.clone() for y in step(i)] for i in range(2)]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=torch.cuda.Stream()):
+            outs.append(step(i))
+        graphs.append(g)
+    for i in (0, 1, 1, 0, 1, 0, 0):
+        for y in outs[i]:
+            y.zero_()
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        for k, (y, e) in enumerate(zip(outs[i], eager[i])):
+            assert torch.equal(y, e), f"graph {i}, output {k}"
+    for h in (r, n, m):
+        h.close()
+
+
 def test_two_handles_on_two_streams():
     """Calls on separate handles may run at the same time: the bits of the same calls in turn."""
     B, T, H, d = 1, 4000, 2, 64

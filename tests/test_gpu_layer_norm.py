@@ -112,14 +112,19 @@ def test_weight_without_bias_and_gradients_not_wanted():
                 assert (y == 5).all() if i == k else torch.equal(y, want)
 
 
-@pytest.mark.parametrize("S", [1, 45])
-def test_nan_stays_in_its_group(S):
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("S", [1, 45, 4001])
+def test_nan_and_infinity_stay_in_their_group(S, value):
     x = lo.cuda(inputs(38, 4, S, 64))
-    x["x"][2, S // 2, 20] = float("nan")
+    x["x"][2, S // 2, 20] = value
     with gb.GroupNorm(64, 4, max_N=4) as n:
-        out, _ = n.forward(x["x"], x["w"], x["b"])
-    bad = torch.isnan(out)
-    assert bad[2, :, 16:32].all() and int(bad.sum()) == S * 16
+        out, stats = n.forward(x["x"], x["w"], x["b"])
+        dx, dw, db = n.backward(x["x"], x["w"], x["b"], stats, x["dout"])
+    for y in (out, dx):
+        bad = torch.isnan(y)
+        assert bad[2, :, 16:32].all() and int(bad.sum()) == S * 16
+    for y in (dw, db):
+        assert torch.isnan(y[16:32]).all() and torch.isfinite(y[:16]).all() and torch.isfinite(y[32:]).all()
 
 
 def test_frames_with_any_dimensions_between():
