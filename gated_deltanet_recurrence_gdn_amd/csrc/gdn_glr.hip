@@ -655,7 +655,7 @@ int waves_of(const GlrArgs &a, int R) { return (int)std::min<long long>(WAVES, (
 // Long tiles only where calls have whole ones and they fill the device twice over (two
 // blocks fit on a CU): below that they leave waves or CUs idle.
 bool fills(const GlrArgs &a, int R) {
-    return a.T >= WAVES * R && slabs_of(a.B, a.H, a.d) * ((a.T + WAVES * R - 1) / (WAVES * R)) >= 2LL * a.ncu;
+    return a.T >= WAVES * R && slabs_of(a.B, a.H, a.d) * ((a.T + WAVES * R - 1) / (WAVES * R)) >= 4LL * a.ncu;
 }
 
 bool few_slabs(const GlrArgs &a, int R) { return slabs_of(a.B, a.H, a.d) <= FEW && a.T > WAVES * R; }

@@ -819,9 +819,9 @@ int blocks_for(int ncu, int threads) { return std::max(1, 16 * ncu * 64 / thread
 
 Split split_for(const GroupNormArgs &a, const Layout &l, long long samples) {
     const long long want = std::max<long long>(1, (blocks_for(a.ncu, l.threads) + samples - 1) / samples);
-    const long long least = (long long)l.R * ROWS_U;  // rows worth a block
+    const long long least = (long long)l.R * ROWS_U;  // rows of a round: stretches are whole rounds
     Split s;
-    s.len = std::max(least, (a.S + want - 1) / want);
+    s.len = (std::max(least, (a.S + want - 1) / want) + least - 1) / least * least;
     s.count = (int)((a.S + s.len - 1) / s.len);
     return s;
 }

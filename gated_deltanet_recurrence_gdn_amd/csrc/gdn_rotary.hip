@@ -228,13 +228,15 @@ __global__ __launch_bounds__(THREADS) void rotary_kernel(RotaryArgs a) {
 
 template <int IO, int W>
 hipError_t launch(const RotaryArgs &a, hipStream_t s) {
-    // Four tokens share a block's passes over the angles and its barriers; one each where that
-    // would leave CUs idle (rows below 4 blocks of 4 tokens a CU).
+    // Four tokens share a block's passes over the angles and its barriers where a token alone
+    // would leave threads idle (6,240 tokens of 4 heads of 128: 7.6 us, one token at a time
+    // 10.8).  One token at a time for wide rows (2 x 32,760 of 64 heads: 381 us, by fours 406) and
+    // where fours would leave CUs idle (1,560 of 40 heads: 8.2 us, by fours 11.3).
     const long long rows = a.B * a.T;
-    if (rows >= 4096)
+    if (rows >= 4096 && a.H * (long long)a.d < 8 * 4 * THREADS)
         rotary_kernel<IO, W, 4><<<dim3((unsigned)std::min<long long>((rows + 3) / 4, ROTARY_BLOCKS)), dim3(THREADS), 0, s>>>(a);
     else
-        rotary_kernel<IO, W, 1><<<dim3((unsigned)rows), dim3(THREADS), 0, s>>>(a);
+        rotary_kernel<IO, W, 1><<<dim3((unsigned)std::min<long long>(rows, 4 * ROTARY_BLOCKS)), dim3(THREADS), 0, s>>>(a);
     return hipGetLastError();
 }
 
