@@ -196,7 +196,10 @@ struct Pair<IO_F32> {
     __device__ __forceinline__ void load(const char *row, unsigned c) { r = *reinterpret_cast<const float2 *>(row + c * 4); }
     __device__ __forceinline__ void zero() { r = make_float2(0.0f, 0.0f); }
     __device__ __forceinline__ float2 get() const { return r; }
-    static __device__ __forceinline__ void store(char *row, unsigned c, float2 x) { *reinterpret_cast<float2 *>(row + c * 4) = x; }
+    static __device__ __forceinline__ void store(char *row, unsigned c, float2 x) {
+        const f32x2_t v = {x.x, x.y};
+        stream_out(reinterpret_cast<f32x2_t *>(row + c * 4), v);
+    }
 };
 template <>
 struct Pair<IO_BF16> {
@@ -206,7 +209,7 @@ struct Pair<IO_BF16> {
     __device__ __forceinline__ void zero() { r = 0; }
     __device__ __forceinline__ float2 get() const { return make_float2(bf16_lo(r), bf16_hi(r)); }
     static __device__ __forceinline__ void store(char *row, unsigned c, float2 x) {
-        *reinterpret_cast<uint32_t *>(row + c * 2) = pack_bf16x2(x.x, x.y);
+        stream_out(reinterpret_cast<uint32_t *>(row + c * 2), pack_bf16x2(x.x, x.y));
     }
 };
 template <>

@@ -87,10 +87,10 @@ __device__ __forceinline__ void store_part(void *row, size_t i, const float (&f)
         part x;
 #pragma unroll
         for (int k = 0; k < W; ++k) x[k] = f[k];
-        *reinterpret_cast<part *>(static_cast<float *>(row) + i) = x;
+        stream_out(reinterpret_cast<part *>(static_cast<float *>(row) + i), x);
     } else {
-        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(row) + i) =
-            make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+        const u32x2_t x = {pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3])};
+        stream_out(reinterpret_cast<u32x2_t *>(static_cast<uint16_t *>(row) + i), x);
     }
 }
 
