@@ -49,7 +49,16 @@ __device__ __forceinline__ void stream_out(T *p, T x) {
     __builtin_nontemporal_store(x, p);
 }
 
-// Eight neighbouring elements, as they lie in memory; i counts vectors.
+// The same hint for inputs that a call reads once (rows of 32 groups normalised: 201 us against
+// 209).  Where a second pass reads them again it costs more than it gives (the norm's training
+// step on two clips: 115 us against 107).
+template <typename T>
+__device__ __forceinline__ T stream_in(const T *p) {
+    return __builtin_nontemporal_load(p);
+}
+
+// Eight neighbouring elements, as they lie in memory; i counts vectors.  load_once: read by no
+// later pass of the call.
 template <int IO>
 struct Vec;
 template <>
@@ -58,6 +67,11 @@ struct Vec<IO_F32> {
     __device__ __forceinline__ void load(const void *p, size_t i) {
         r[0] = static_cast<const float4 *>(p)[2 * i];
         r[1] = static_cast<const float4 *>(p)[2 * i + 1];
+    }
+    __device__ __forceinline__ void load_once(const void *p, size_t i) {
+        const f32x4_t a = stream_in(static_cast<const f32x4_t *>(p) + 2 * i), b = stream_in(static_cast<const f32x4_t *>(p) + 2 * i + 1);
+        r[0] = make_float4(a[0], a[1], a[2], a[3]);
+        r[1] = make_float4(b[0], b[1], b[2], b[3]);
     }
     __device__ __forceinline__ void get(float (&f)[8]) const {
         f[0] = r[0].x; f[1] = r[0].y; f[2] = r[0].z; f[3] = r[0].w;
@@ -73,6 +87,10 @@ template <>
 struct Vec<IO_BF16> {
     uint4 r;
     __device__ __forceinline__ void load(const void *p, size_t i) { r = static_cast<const uint4 *>(p)[i]; }
+    __device__ __forceinline__ void load_once(const void *p, size_t i) {
+        const u32x4_t v = stream_in(static_cast<const u32x4_t *>(p) + i);
+        r = make_uint4(v[0], v[1], v[2], v[3]);
+    }
     __device__ __forceinline__ void get(float (&f)[8]) const {
         f[0] = bf16_lo(r.x); f[1] = bf16_hi(r.x); f[2] = bf16_lo(r.y); f[3] = bf16_hi(r.y);
         f[4] = bf16_lo(r.z); f[5] = bf16_hi(r.z); f[6] = bf16_lo(r.w); f[7] = bf16_hi(r.w);
@@ -86,6 +104,10 @@ template <>
 struct Vec<IO_FP8> {
     uint2 r;
     __device__ __forceinline__ void load(const void *p, size_t i) { r = static_cast<const uint2 *>(p)[i]; }
+    __device__ __forceinline__ void load_once(const void *p, size_t i) {
+        const u32x2_t v = stream_in(static_cast<const u32x2_t *>(p) + i);
+        r = make_uint2(v[0], v[1]);
+    }
     __device__ __forceinline__ void get(float (&f)[8]) const {
         fp8x4_to_f32(r.x, f);
         fp8x4_to_f32(r.y, f + 4);

@@ -100,7 +100,7 @@ __global__ __launch_bounds__(512) void rows_forward_kernel(GroupNormArgs a, int 
 #pragma unroll
         for (int u = 0; u < ROWS_U; ++u) {
             const long long n = n0 + u * step + row;
-            if (row < R && n < a.N) x[u].load(a.x, (size_t)n * V + col);
+            if (row < R && n < a.N) x[u].load_once(a.x, (size_t)n * V + col);
         }
 #pragma unroll
         for (int u = 0; u < ROWS_U; ++u) {
@@ -168,8 +168,8 @@ __global__ __launch_bounds__(512) void rows_backward_kernel(GroupNormArgs a, int
         for (int u = 0; u < U; ++u) {
             const long long n = n0 + u * step + row;
             if (row < R && n < a.N) {
-                x[u].load(a.x, (size_t)n * V + col);
-                y[u].load(a.dout, (size_t)n * V + col);
+                x[u].load_once(a.x, (size_t)n * V + col);
+                y[u].load_once(a.dout, (size_t)n * V + col);
                 st[u] = reinterpret_cast<const float2 *>(a.stats)[(size_t)n * a.G + col / P];
             }
         }

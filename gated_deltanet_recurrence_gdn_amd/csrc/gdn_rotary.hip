@@ -62,7 +62,7 @@ template <int IO, int W>
 __device__ __forceinline__ void load_part(const void *row, size_t i, float (&f)[W]) {
     if constexpr (W == 8) {
         Vec<IO> x;
-        x.load(row, i / 8);
+        x.load_once(row, i / 8);
         x.get(f);
     } else if constexpr (IO == IO_F32) {
         typedef float part __attribute__((ext_vector_type(W)));
@@ -140,7 +140,7 @@ __global__ __launch_bounds__(THREADS) void rotary_kernel(RotaryArgs a) {
             while (k < tokens) {
                 Vec<IO> x;
                 float f[8];
-                x.load(from[k], v);
+                x.load_once(from[k], v);
                 x.get(f);
                 const int j0 = c * 4;
 #pragma unroll
@@ -195,7 +195,7 @@ __global__ __launch_bounds__(THREADS) void rotary_kernel(RotaryArgs a) {
                 for (unsigned e = threadIdx.x; e < n * V; e += THREADS) {
                     const unsigned u = e / V, k = TOK == 1 ? 0 : (u0 + u) / a.H, h = u0 + u - k * a.H;
                     Vec<IO> x;
-                    x.load(from[k], h * V + (e - u * V));
+                    x.load_once(from[k], h * V + (e - u * V));
                     reinterpret_cast<Vec<IO> *>(stage)[e] = x;
                 }
                 __syncthreads();
