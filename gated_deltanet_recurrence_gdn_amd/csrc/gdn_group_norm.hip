@@ -17,6 +17,10 @@
 // (count, mean, squares around it) are joined by
 //     mean = sum n_i mean_i / n,   squares = sum squares_i + sum n_i (mean_i - mean)^2,
 // so that means far from zero cost no precision.  Everything is fp32 until the last rounding.
+// Measured (a copy of 1 GB: 5.1 TB/s): rows, 65,520 x 4096 in 32 groups, SiLU, bf16: 201 us,
+// 5.3 TB/s (its gradient 350 us, 4.6 TB/s; joined through LDS instead: 585 us forward); split,
+// 2 x 32,760 x 512 forward 44 us and gradient 66 us with both passes over x and dout; resident,
+// 3 x 77 x 320 fp32: 9 and 14 us, a block for each sample.
 #include "gdn_elem.h"
 #include "gdn_layer.h"
 
@@ -28,7 +32,9 @@ namespace {
 constexpr int RES_K = 4;        // rows of a thread in the resident form
 constexpr int ROWS_U = 4;       // rows a thread of the other forms has in flight
 constexpr int BATCH = 1024;     // samples of one round of the split form (bounds the workspace)
-constexpr int JOIN_HERE = 2048; // stretches times groups of a sample that each block may join for itself
+// Stretches times groups of a sample that each block may join for itself: saves a launch (20 x
+// 1,798 x 256, 52 stretches of 16 groups: 19.9 us against 21.8).
+constexpr int JOIN_HERE = 2048;
 
 // 1 / (1 + e^-z) with the hardware's exponential and reciprocal (an ulp each; the IEEE
 // forms would make the pass bound by the vector units).
@@ -858,8 +864,8 @@ template <int IO, bool SILU>
 hipError_t forward(const GroupNormArgs &a, hipStream_t s) {
     if (const int L = rows_lanes(a)) {
         const Layout l = rows_layout(a, L);
-        // 24 waves a CU, where 16 to 20 fit at once: 65,520 x 4096 bf16 takes 220 us, with 16
-        // waves 240, with 64 or 128 waves 232 to 235
+        // 24 waves a CU, where 16 to 20 fit at once: at 65,520 x 4096 in bf16 16 waves are 9%
+        // slower, 64 or 128 waves 5 to 7%
         const long long blocks = std::min<long long>((a.N + l.R - 1) / l.R, blocks_for(a.ncu, l.threads) * 3 / 2);
         rows_forward_kernel<IO, SILU><<<dim3((unsigned)blocks), dim3(l.threads), 0, s>>>(a, l.V, l.R, L);
         return hipGetLastError();

@@ -10,11 +10,12 @@
 //  * halves that are multiples of W elements, W * size >= 8 bytes: a lane takes W neighbouring
 //    elements of a section's first half and the W of the second half that belong to them.
 //  * other halves: whole heads are staged in LDS in 16-byte vectors; a lane forms eight
-//    neighbouring outputs and finds their partners there.  (Two-byte accesses to memory
-//    instead: 1.3 TB/s where this has
-//    2.9 TB/s, at 2 x 11,267 tokens of 26 heads of 64 in bf16.)
+//    neighbouring outputs and finds their partners there (2 x 11,267 tokens of 26 heads of 64,
+//    halves of 2, 4 and 3, bf16: 57 us; two-byte accesses to memory instead: 116 us).
 // out may be x: a pair is read and written by one lane, and heads are staged whole before any
 // of them is written.
+// Measured: 2 x 32,760 tokens of 64 heads of 128 in packed rows, bf16: 358 us, 6.0 TB/s read
+// and written (a copy of 1 GB: 5.1 TB/s); 8 tokens of 40 heads: 4.3 us, the latency of one block.
 #include "gdn_elem.h"
 #include "gdn_layer.h"
 
@@ -230,7 +231,7 @@ template <int IO, int W>
 hipError_t launch(const RotaryArgs &a, hipStream_t s) {
     // Four tokens share a block's passes over the angles and its barriers where a token alone
     // would leave threads idle (6,240 tokens of 4 heads of 128: 7.6 us, one token at a time
-    // 10.8).  One token at a time for wide rows (2 x 32,760 of 64 heads: 381 us, by fours 406) and
+    // 10.8).  One token at a time for wide rows (2 x 32,760 of 64 heads: fours are 7% slower) and
     // where fours would leave CUs idle (1,560 of 40 heads: 8.2 us, by fours 11.3).
     const long long rows = a.B * a.T;
     if (rows >= 4096 && a.H * (long long)a.d < 8 * 4 * THREADS)
