@@ -8,8 +8,9 @@
 //  * rows (S = 1, D = C / G channels of a group a multiple of 8 up to 512): a group is D / 8
 //    lanes of a wave, or the power of two above with the rest idle; its sums are exchanges
 //    between lanes and the row is read once.
-//  * resident (small samples): a block has a sample, in registers for the forward pass, and
-//    joins its groups through LDS; one launch.
+//  * resident (small samples): a block has a sample, or a piece of it of whole groups where
+//    samples are few, in registers for the forward pass, and joins its groups through LDS; one
+//    launch.
 //  * split (larger samples): a sample is cut into stretches of rows.  One launch forms each
 //    stretch's sums, a small one joins them, one applies them, taking the stretches in the
 //    opposite order so that what the first left in the caches is read from there.
@@ -20,11 +21,13 @@
 // Measured (a copy of 1 GB: 5.1 TB/s): rows, 65,520 x 4096 in 32 groups, SiLU, bf16: 201 us,
 // 5.3 TB/s (its gradient 350 us, 4.6 TB/s; joined through LDS instead: 585 us forward); split,
 // 2 x 32,760 x 512 forward 44 us and gradient 66 us with both passes over x and dout; resident,
-// 3 x 77 x 320 fp32: 9 and 14 us, a block for each sample.
+// 3 x 77 x 320 fp32: 6 us forward and 11 us with the gradient's two launches, 8 pieces a sample
+// (whole samples: 9 and 16 us).
 #include "gdn_elem.h"
 #include "gdn_layer.h"
 
 #include <algorithm>
+#include <numeric>
 
 namespace gdn {
 namespace {
@@ -139,16 +142,31 @@ __device__ __forceinline__ void put8(float *lds, int i, const float (&f)[8]) {
     reinterpret_cast<float4 *>(lds)[2 * i + 1] = make_float4(f[4], f[5], f[6], f[7]);
 }
 
-// Sums of a block's rows per channel: part[blockIdx.x][0 .. C) gets s1, [C .. 2C) s2.
-__device__ __forceinline__ void block_channels(const float (&s1)[8], const float (&s2)[8], float *lds, float *part, int C,
-                                               int row, int col, int R) {
+// Sums of a block's rows for each of its C channels: part[0 .. C) gets s1, part[stride ..
+// stride + C) s2.  Many rows are first summed by P threads a channel to P rows, the square root
+// of R as far as the block has threads for them (204 rows of 40 channels: 2 us less; 89 rows:
+// 0.3 us more, for the barrier).
+__device__ __forceinline__ void block_channels(const float (&s1)[8], const float (&s2)[8], float *lds, float *part, int stride,
+                                               int C, int row, int col, int R) {
+    int P = 1;
+    while (R > 128 && P * P < R && (P + 1) * C <= (int)blockDim.x) ++P;
     for (int k = 0; k < 2; ++k) {
         if (row < R) put8(lds + row * C, col, k ? s2 : s1);
         __syncthreads();
+        if (P > 1) {
+            if ((int)threadIdx.x < P * C) {
+                float s = 0.0f;
+#pragma unroll 4
+                for (int i = threadIdx.x; i < R * C; i += P * C) s += lds[i];
+                lds[threadIdx.x] = s;  // row threadIdx.x / C, which this thread alone reads
+            }
+            __syncthreads();
+        }
+        const int rows = P > 1 ? P : R;
         for (int c = threadIdx.x; c < C; c += blockDim.x) {
             float s = lds[c];
-            for (int r = 1; r < R; ++r) s += lds[r * C + c];
-            part[(size_t)blockIdx.x * 2 * C + k * C + c] = s;
+            for (int r = 1; r < rows; ++r) s += lds[r * C + c];
+            part[(size_t)k * stride + c] = s;
         }
         __syncthreads();
     }
@@ -204,7 +222,7 @@ __global__ __launch_bounds__(512) void rows_backward_kernel(GroupNormArgs a, int
             if (in && a.dx) OutVec<IO>::store(a.dx, (size_t)n * V + col, t);
         }
     }
-    if (part) block_channels(sb, sw, lds, part, a.C, on ? row : R, col, R);
+    if (part) block_channels(sb, sw, lds, part + (size_t)blockIdx.x * 2 * a.C, a.C, a.C, on ? row : R, col, R);
 }
 
 // ---- joining a block's threads by group ---------------------------------------------
@@ -336,22 +354,39 @@ __device__ __forceinline__ void sum_groups(const float *lds, int R, int C, int D
 
 // ---- resident -----------------------------------------------------------------------
 
-// A block takes samples blockIdx.x, + gridDim.x, ...; thread (row, col) has rows row + k R.
-// LDS: 2 R C floats for joining, then 2 G for the groups' results.
+// The call as piece p sees it, C channels in G groups.
+template <int IO>
+__device__ __forceinline__ void to_piece(GroupNormArgs &a, int p, int C, int G) {
+    const size_t c = (size_t)p * C;
+    a.x = at<IO>(a.x, c);
+    if (a.weight) a.weight += c;
+    if (a.bias) a.bias += c;
+    if (a.out) a.out = at<OutIo<IO>>(a.out, c);
+    if (a.dout) a.dout = at<OutIo<IO>>(a.dout, c);
+    if (a.dx) a.dx = at<OutIo<IO>>(a.dx, c);
+    if (a.stats) a.stats += 2 * p * G;
+    if (a.stats_out) a.stats_out += 2 * p * G;
+}
+
+// A block takes a piece of V vectors (whole groups; piece blockIdx.y) of samples blockIdx.x,
+// + gridDim.x, ...; thread (row, col) has rows row + k R.  LDS: 2 R C floats for joining (C, G:
+// the piece's channels and groups), then 2 G for the groups' results.
 template <int IO, bool SILU>
 __global__ __launch_bounds__(1024) void resident_forward_kernel(GroupNormArgs a, int V, int R) {
     extern __shared__ float lds[];
-    const int row = threadIdx.x / V, col = threadIdx.x % V, C = a.C, D = C / a.G, S = (int)a.S;
+    const int row = threadIdx.x / V, col = threadIdx.x % V, C = 8 * V, D = a.C / a.G, S = (int)a.S;
+    const int width = a.C / 8;
+    to_piece<IO>(a, blockIdx.y, C, C / D);
     const bool on = row < R;
     float2 *group = reinterpret_cast<float2 *>(lds + 2 * R * C);
     const Share share(S, R);
     const int unit = unit_of(D);
     for (long long n = blockIdx.x; n < a.N; n += gridDim.x) {
         Vec<IO> x[RES_K];
-        const size_t base = (size_t)n * S * V + col;
+        const size_t base = (size_t)n * S * width + col;
 #pragma unroll
         for (int k = 0; k < RES_K; ++k)
-            if (on && row + k * R < S) x[k].load(a.x, base + (size_t)(row + k * R) * V);
+            if (on && row + k * R < S) x[k].load(a.x, base + (size_t)(row + k * R) * width);
         if (on) {
             float mean[8] = {}, sq[8] = {};
             const float inv = row < S ? 1.0f / share(row) : 0.0f;
@@ -396,7 +431,7 @@ __global__ __launch_bounds__(1024) void resident_forward_kernel(GroupNormArgs a,
                     x[k].get(f);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) f[i] = act<SILU>(fmaf((f[i] - st[i].x) * st[i].y, w[i], b[i]));
-                    OutVec<IO>::store(a.out, base + (size_t)(row + k * R) * V, f);
+                    OutVec<IO>::store(a.out, base + (size_t)(row + k * R) * width, f);
                 }
         }
         __syncthreads();  // the next sample writes what is read above
@@ -408,7 +443,9 @@ __global__ __launch_bounds__(1024) void resident_forward_kernel(GroupNormArgs a,
 template <int IO, bool SILU>
 __global__ __launch_bounds__(1024) void resident_backward_kernel(GroupNormArgs a, int V, int R, float *part) {
     extern __shared__ float lds[];
-    const int row = threadIdx.x / V, col = threadIdx.x % V, C = a.C, D = C / a.G, S = (int)a.S;
+    const int row = threadIdx.x / V, col = threadIdx.x % V, C = 8 * V, D = a.C / a.G, S = (int)a.S;
+    const int width = a.C / 8;
+    to_piece<IO>(a, blockIdx.y, C, C / D);
     const bool on = row < R;
     const int unit = unit_of(D);
     float2 *group = reinterpret_cast<float2 *>(lds + 2 * R * C);
@@ -419,7 +456,7 @@ __global__ __launch_bounds__(1024) void resident_backward_kernel(GroupNormArgs a
         channel8(b, a.bias, col, 0.0f);
     }
     for (long long n = blockIdx.x; n < a.N; n += gridDim.x) {
-        const size_t base = (size_t)n * S * V + col;
+        const size_t base = (size_t)n * S * width + col;
         float2 st[8];
         if (on) {
 #pragma unroll
@@ -430,8 +467,8 @@ __global__ __launch_bounds__(1024) void resident_backward_kernel(GroupNormArgs a
                 Vec<IO> x;
                 OutVec<IO> y;
                 float f[8], t[8];
-                x.load(a.x, base + (size_t)r * V);
-                y.load(a.dout, base + (size_t)r * V);
+                x.load(a.x, base + (size_t)r * width);
+                y.load(a.dout, base + (size_t)r * width);
                 x.get(f);
                 y.get(t);
 #pragma unroll
@@ -462,8 +499,8 @@ __global__ __launch_bounds__(1024) void resident_backward_kernel(GroupNormArgs a
                 Vec<IO> x;
                 OutVec<IO> y;
                 float f[8], t[8];
-                x.load(a.x, base + (size_t)r * V);
-                y.load(a.dout, base + (size_t)r * V);
+                x.load(a.x, base + (size_t)r * width);
+                y.load(a.dout, base + (size_t)r * width);
                 x.get(f);
                 y.get(t);
 #pragma unroll
@@ -471,12 +508,12 @@ __global__ __launch_bounds__(1024) void resident_backward_kernel(GroupNormArgs a
                     const float xh = (f[i] - st[i].x) * st[i].y, dz = act_grad<SILU>(t[i], fmaf(xh, w[i], b[i]));
                     t[i] = st[i].y * (dz * w[i] - m[i].x - xh * m[i].y);
                 }
-                OutVec<IO>::store(a.dx, base + (size_t)r * V, t);
+                OutVec<IO>::store(a.dx, base + (size_t)r * width, t);
             }
         }
         __syncthreads();  // the next sample writes what is read above
     }
-    if (part) block_channels(sb, sw, lds, part, C, row, col, R);
+    if (part) block_channels(sb, sw, lds, part + (size_t)blockIdx.x * 2 * a.C + blockIdx.y * C, a.C, C, row, col, R);
 }
 
 // ---- split --------------------------------------------------------------------------
@@ -690,7 +727,7 @@ __global__ __launch_bounds__(1024) void split_sums_kernel(GroupNormArgs a, int V
                 }
         }
     }
-    block_channels(s1, s2, lds, part + (size_t)blockIdx.y * sp.count * 2 * a.C, a.C, row, col, R);
+    block_channels(s1, s2, lds, part + ((size_t)blockIdx.y * sp.count + blockIdx.x) * 2 * a.C, a.C, a.C, row, col, R);
 }
 
 template <int IO, bool SILU>
@@ -807,16 +844,38 @@ Layout rows_layout(const GroupNormArgs &a, int L) {
     return l;
 }
 
-// At most RES_K rows of a thread.  A sample that fits is faster here than split even if it is
-// alone (3 x 77 x 320 fp32, forward and backward: 27 us, split 37 us: two launches more each).
-bool resident_form(const GroupNormArgs &a) { return a.S <= RES_K * (1024 / (a.C / 8)); }
+// Pieces of a sample in the resident form, which takes blocks of their own: whole groups and
+// vectors, as many as even parts of at least PIECE vectors (128 bytes of fp32) allow while
+// samples alone leave CUs idle.
+constexpr int PIECE = 4, WIDE = 128;
+int pieces(const GroupNormArgs &a) {
+    const int V = a.C / 8, D = a.C / a.G, parts = V / (D / std::gcd(D, 8));  // of whole groups and vectors
+    int p = (int)std::min<long long>({parts, V / PIECE, a.ncu / std::max<long long>(a.N, 1)});
+    while (p > 1 && parts % p) --p;
+    return std::max(p, 1);
+}
 
-// Threads of the resident form: few for small samples, RES_K vectors each for large ones.
-Layout resident_layout(const GroupNormArgs &a) {
-    const long long vectors = a.S * (a.C / 8);
+// At most RES_K rows of a thread.  What fits is faster here than split even if a sample is
+// alone in one piece, and faster in pieces (3 x 77 x 320 fp32, forward and backward: 17 us in 8
+// pieces, 25 whole; 8 x 200 x 1280 in 32 pieces 27 us, split 39; forward only, 1 x 800 x 512 in
+// 16 pieces 9.6 us, split 12.3).  The gradient's two passes of few blocks take longer than the
+// split form's many: beyond whole samples that fit and half a row a thread it wants most CUs
+// busy, or rows so wide that a split block has one or two at a time (3 x 400 x 320: in pieces
+// 18 us, split 14; 8 x 400 x 1280: 20 us, split 29; 2 x 77 x 4096: 14 us, split 23).
+bool resident_form(const GroupNormArgs &a, int p, bool gradient) {
+    const int V = a.C / 8;
+    if (a.S > RES_K * (1024 / (V / p))) return false;
+    return !gradient || a.S <= RES_K * (1024 / V) || a.S * (V / p) <= 512 || V >= WIDE ||
+           4 * p * a.N >= 3LL * a.ncu;
+}
+
+// Threads of the resident form for rows of V vectors: few for small samples, RES_K vectors each
+// for large ones.
+Layout resident_layout(const GroupNormArgs &a, int V) {
+    const long long vectors = a.S * V;
     long long t = std::max<long long>(64, std::min<long long>(1024, (vectors + 63) / 64 * 64));
-    Layout l = layout(a.C, (int)t);
-    while ((long long)l.R * RES_K < a.S) l = layout(a.C, l.threads + 64);  // a row's width may not divide
+    Layout l = layout(8 * V, (int)t);
+    while ((long long)l.R * RES_K < a.S) l = layout(8 * V, l.threads + 64);  // a row's width may not divide
     return l;
 }
 
@@ -870,13 +929,13 @@ hipError_t forward(const GroupNormArgs &a, hipStream_t s) {
         rows_forward_kernel<IO, SILU><<<dim3((unsigned)blocks), dim3(l.threads), 0, s>>>(a, l.V, l.R, L);
         return hipGetLastError();
     }
-    if (resident_form(a)) {
-        const Layout l = resident_layout(a);
-        const size_t lds = (2 * (size_t)l.R * a.C + 2 * a.G) * sizeof(float);
+    if (const int p = pieces(a); resident_form(a, p, false)) {
+        const Layout l = resident_layout(a, a.C / 8 / p);
+        const size_t lds = (2 * (size_t)l.R * 8 * l.V + 2 * (a.G / p)) * sizeof(float);
         const long long blocks = std::min<long long>(a.N, 1 << 20);
         const hipError_t e = allow_lds(reinterpret_cast<const void *>(&resident_forward_kernel<IO, SILU>), lds);
         if (e != hipSuccess) return e;
-        resident_forward_kernel<IO, SILU><<<dim3((unsigned)blocks), dim3(l.threads), lds, s>>>(a, l.V, l.R);
+        resident_forward_kernel<IO, SILU><<<dim3((unsigned)blocks, p), dim3(l.threads), lds, s>>>(a, l.V, l.R);
         return hipGetLastError();
     }
     const Layout l = layout(a.C, 256);
@@ -919,13 +978,13 @@ hipError_t backward(const GroupNormArgs &a, hipStream_t s) {
             a, l.V, l.R, L, wanted ? w.part : nullptr);
         return wanted ? channels(a, w.part, blocks, s) : hipGetLastError();
     }
-    if (resident_form(a)) {
-        const Layout l = resident_layout(a);
-        const size_t lds = (2 * (size_t)l.R * a.C + 2 * a.G) * sizeof(float);
+    if (const int p = pieces(a); resident_form(a, p, true)) {
+        const Layout l = resident_layout(a, a.C / 8 / p);
+        const size_t lds = (2 * (size_t)l.R * 8 * l.V + 2 * (a.G / p)) * sizeof(float);
         const int blocks = (int)std::min<long long>(a.N, blocks_for(a.ncu, l.threads));
         const hipError_t e = allow_lds(reinterpret_cast<const void *>(&resident_backward_kernel<IO, SILU>), lds);
         if (e != hipSuccess) return e;
-        resident_backward_kernel<IO, SILU><<<dim3(blocks), dim3(l.threads), lds, s>>>(a, l.V, l.R, wanted ? w.part : nullptr);
+        resident_backward_kernel<IO, SILU><<<dim3(blocks, p), dim3(l.threads), lds, s>>>(a, l.V, l.R, wanted ? w.part : nullptr);
         return wanted ? channels(a, w.part, blocks, s) : hipGetLastError();
     }
     const Layout l = layout(a.C, 256);

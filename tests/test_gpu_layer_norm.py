@@ -71,6 +71,16 @@ def test_one_large_value(N, S, C, G):
     parity("outlier", x, G, dtype="fp32")
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp8"])
+@pytest.mark.parametrize("N,S,C,G", [
+    (3, 77, 320, 32), (1, 102, 320, 32), (3, 816, 320, 32), (3, 817, 320, 32),  # 8 pieces of 4 groups of 10
+    (1, 5, 240, 80), (2, 40, 240, 80), (3, 600, 1280, 32), (2, 77, 4096, 32), (1, 900, 8192, 512), (1, 260, 8192, 8),
+    (85, 30, 96, 3), (86, 30, 96, 3), (128, 20, 512, 32), (129, 20, 512, 32), (256, 9, 64, 4), (1, 2, 64, 64),
+])
+def test_pieces_of_few_samples(dtype, N, S, C, G):
+    parity("pieces", inputs(49, N, S, C, dtype), G, dtype=dtype)
+
+
 @pytest.mark.parametrize("value", [0.0, 10.0, -2.0 ** -20])
 def test_constant_groups(value):
     x = inputs(35, 2, 600, 32, "fp32")
