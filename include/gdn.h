@@ -257,8 +257,9 @@ int gdn_forward_noalloc(const gdn_config *cfg, const void *q, const void *k,
  * where pair i is elements (2i, 2i + 1) of the section, or (i, i +
  * axis_dim[s] / 2) with GDN_ROTARY_HALVES.  GDN_ROTARY_INVERSE turns by the
  * negative angles: the inverse, and the gradient with respect to x.  Angles are
- * formed and reduced in 64 bits (positions far from 0 lose nothing); the turn
- * is fp32, rounded once.
+ * formed and reduced in 64 bits (off by up to 2^-50 of their size: below 2^-24,
+ * half a step of fp32 at 1, for positions up to 2^26); the turn is fp32, rounded
+ * once.
  *
  * The turn keeps a pair's length, so q and k may be turned before the L2
  * normalisation of gdn_forward_packed: turn the first 2 H heads of the packed
@@ -342,7 +343,8 @@ int gdn_glr_create(const gdn_glr_config *cfg, gdn_handle *out_h);
 /*
  * state_in NULL = zeros; state_out NULL = discarded, may equal state_in; saved
  * NULL = not wanted (needed by gdn_glr_backward).  T = 0: state_out receives
- * state_in or zeros.  No NaN or infinity is looked for: they propagate.
+ * state_in or zeros.  No NaN or infinity is looked for: they propagate, through
+ * a_t = 0 too (0 times them is NaN), so tokens of padding need finite values.
  */
 int gdn_glr_forward(gdn_handle h, const void *v, const float *beta, const float *decay,
                     const float *state_in, float *state_out, float *saved, void *out,
