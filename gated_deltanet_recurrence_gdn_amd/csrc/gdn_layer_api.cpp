@@ -215,7 +215,7 @@ int gn_check_sizes(gdn_ctx *h, long long N, long long S) {
     if (N < 0 || S < 0) return fail(h, GDN_ERR_ARG, "N = %lld and S = %lld must be >= 0", N, S);
     if (N > h->gn.max_N) return fail(h, GDN_ERR_ARG, "N = %lld exceeds max_N = %lld", N, h->gn.max_N);
     if (S > (1LL << 30)) return fail(h, GDN_ERR_UNSUPPORTED, "S = %lld exceeds 2^30", S);
-    if ((double)N * (double)S * h->gn.C * sizeof(float) > 9.0e18)
+    if ((double)N * (double)S * h->gn.C * sizeof(float) >= 4611686018427387904.0)  // 2^62
         return fail(h, GDN_ERR_ARG, "the extent of N * S * C = %lld * %lld * %d values is too large", N, S, h->gn.C);
     return GDN_OK;
 }

@@ -392,7 +392,7 @@ typedef struct {
  * owns a workspace that its calls share (see Ownership above). */
 int gdn_group_norm_create(const gdn_group_norm_config *cfg, gdn_handle *out_h);
 
-/* S at most 2^30, 4 N S C bytes at most 9e18.  stats NULL = not wanted (needed by
+/* S at most 2^30, 4 N S C below 2^62.  stats NULL = not wanted (needed by
  * gdn_group_norm_backward).  N = 0 or S = 0 writes nothing. */
 int gdn_group_norm_forward(gdn_handle h, const void *x, const float *weight,
                            const float *bias, void *out, float *stats, long long N,
