@@ -432,6 +432,8 @@ def rotary(x, axis_dims, theta=10000.0, positions=None, grid=None, first_token=0
     gradient with respect to x.  out may be x (in place).  Returns out (fp32 for fp32 x, else bf16).
     """
     import torch
+    if len(axis_dims) != 3:
+        raise ValueError(f"axis_dims: expected three sizes (time, height, width), got {axis_dims}")
     io = _io_of(x.dtype)
     odt = torch.float32 if io == GDN_F32 else torch.bfloat16
     device = x.get_device()

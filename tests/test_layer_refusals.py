@@ -1,6 +1,7 @@
 """Calls of the operators around the recurrence that are refused for their extents or their
 arguments together, without a GPU."""
 import pytest
+import torch
 
 from gated_deltanet_recurrence_gdn_amd import binding as gb
 
@@ -23,3 +24,9 @@ def test_group_norm_extents_beyond_64_bits(C, N, S):
             assert "extent" in gb.gdn_last_error(h)
     finally:
         gb.gdn_free(h)
+
+
+@pytest.mark.parametrize("dims", [(), (4,), (4, 4), (2, 2, 2, 2)])
+def test_rotary_takes_three_axis_sizes(dims):
+    with pytest.raises(ValueError, match="axis_dims"):
+        gb.rotary(torch.zeros((1, 2, 3, 8)), dims, grid=(1, 1))
