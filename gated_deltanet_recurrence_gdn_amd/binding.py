@@ -427,7 +427,8 @@ def rotary(x, axis_dims, theta=10000.0, positions=None, grid=None, first_token=0
     token side by side; q and k of a packed projection are one x of twice the heads).
 
     axis_dims: elements of a head turned by each axis; positions: int32 [B, T, 3] or [T, 3] (the same for
-    every batch element), or None for a raster grid=(height, width) whose first token is first_token.
+    every batch element), or None for a raster grid=(height, width) whose first token is first_token (neither
+    is read where positions are given).
     halves: pairs (i, i + dim/2) instead of (2i, 2i+1).  inverse: the negative angles, which is the
     gradient with respect to x.  out may be x (in place).  Returns out (fp32 for fp32 x, else bf16).
     """
@@ -444,23 +445,27 @@ def rotary(x, axis_dims, theta=10000.0, positions=None, grid=None, first_token=0
         out = torch.empty((B, T, H, d), dtype=odt, device=x.device)
     elif out.shape != x.shape or out.dtype is not odt or out.get_device() != device:
         raise ValueError(f"out: expected {odt} {(B, T, H, d)} on {x.device}, got {out.dtype} {tuple(out.shape)}")
-    if 0 in (B, H, d, T):
-        return out
-    xbs, xts, xhs, xes = x.stride()
-    obs, ots, ohs, oes = out.stride()
-    for name, hs, es in (("x", xhs, xes), ("out", ohs, oes)):
-        if (d > 1 and es != 1) or (H > 1 and hs != d):
-            raise ValueError(f"{name}: the heads of a token must lie side by side, got strides "
-                             f"{(x if name == 'x' else out).stride()}")
-    if T == 1:  # a dimension of one has no stride of its own
-        xts = ots = H * d
-    if B == 1:
+    none = 0 in (B, T, H)
+    if none:  # nothing to read or write: what remains is checked by a call on no tokens
+        B, H = max(B, 1), max(H, 1)
         xbs = obs = 0
+        xts = ots = H * d
+    else:
+        xbs, xts, xhs, xes = x.stride()
+        obs, ots, ohs, oes = out.stride()
+        for name, hs, es in (("x", xhs, xes), ("out", ohs, oes)):
+            if (d > 1 and es != 1) or (H > 1 and hs != d):
+                raise ValueError(f"{name}: the heads of a token must lie side by side, got strides "
+                                 f"{(x if name == 'x' else out).stride()}")
+        if T == 1:  # a dimension of one has no stride of its own
+            xts = ots = H * d
+        if B == 1:
+            xbs = obs = 0
     pbs = 0
     if positions is not None:
         if positions.dtype is not torch.int32 or positions.get_device() != device or not positions.is_contiguous() or \
-                tuple(positions.shape) not in ((T, 3), (B, T, 3)):
-            raise ValueError(f"positions: expected contiguous int32 {(T, 3)} or {(B, T, 3)} on {x.device}, "
+                tuple(positions.shape) not in ((T, 3), (x.shape[0], T, 3)):
+            raise ValueError(f"positions: expected contiguous int32 {(T, 3)} or {(x.shape[0], T, 3)} on {x.device}, "
                              f"got {positions.dtype} {tuple(positions.shape)} on {positions.device}")
         pbs = 3 * T if positions.dim() == 3 else 0
         height = width = 1
@@ -471,7 +476,8 @@ def rotary(x, axis_dims, theta=10000.0, positions=None, grid=None, first_token=0
         height, width = grid
     flags = (GDN_ROTARY_HALVES if halves else 0) | (GDN_ROTARY_INVERSE if inverse else 0)
     cfg = _rotary_config(device, B, H, d, io, tuple(axis_dims), float(theta), flags)
-    st = gdn_rotary(cfg, x, xts, xbs, out, ots, obs, positions, pbs, first_token, height, width, T, _stream_of(device))
+    st = gdn_rotary(cfg, x, xts, xbs, out, ots, obs, positions, pbs, first_token, height, width,
+                    0 if none else T, _stream_of(device))
     if st != GDN_OK:
         raise GDNError(st, gdn_last_error(None))
     return out
