@@ -129,6 +129,15 @@ __device__ float state_before(const Chain &c, Window &win, int i, uint32_t call,
     }
 }
 
+// Between lanes of one wave that write LDS and others that read it (and before it is written
+// anew): the order that the compiler has to keep.  LDS serves a wave's accesses in order, so
+// no instruction comes of it.
+__device__ __forceinline__ void wave_order_lds() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // State before tile k > 0 of channel `c` of the slab; the whole block, lanes l, l + 16, l + 32
 // and l + 48 of wave w for channel 16 w + l.  `base` is the slab's first word of tile k;
 // `share` channels have one word in the plane mul.  (A, H) is the tile's own map.
@@ -185,9 +194,11 @@ __device__ float state_before_by_block(const Chain &ch, Window &win, uint32_t ca
             win.m[4 * u + q][c] = value(wm[u]);
             win.d[4 * u + q][c] = value(wd[u]);
         }
+        wave_order_lds();  // the four lanes of a channel read what all four wrote
         const int n = hi < 16 ? hi : 16;
 #pragma unroll 1
         for (int t = 0; t < n; ++t) s = fmaf(win.m[t][c], s, win.d[t][c]);
+        wave_order_lds();
     }
     return s;
 }
