@@ -6,6 +6,7 @@ Each test states the launch rule that it relies on and asserts that its size tak
 import pytest
 import torch
 
+import layer_bounds as bounds
 import layer_oracle as lo
 from gated_deltanet_recurrence_gdn_amd import binding as gb
 
@@ -67,3 +68,66 @@ def test_long_tiles(dtype, beta, reverse, H, d):
     for name, y in (("dv", dv), ("dbeta", dbeta), ("ddecay", ddecay), ("dstate_in", ds)):
         if y is not None:
             lo.check(name, some(y), *ref[name])
+
+
+# ---- group norm -------------------------------------------------------------------
+
+def check(label, got, ref, bound):
+    """layer_oracle.check on the device."""
+    fi = torch.finfo(got.dtype)
+    tol = bound + fi.eps / 2 * (ref.abs() + bound) + fi.tiny * fi.eps
+    bad = ~((got.double() - ref).abs() <= tol)
+    assert got.shape == ref.shape and not bad.any(), f"{label}: {int(bad.sum())} of {bad.numel()} values off"
+
+
+def norm_inputs(seed, N, S, C, dtype, offset=0.5):
+    g = lo.gen(seed)
+    x = (repeated(g, N, S, C, dtype="fp32") + offset * torch.randn((C,), generator=g).cuda()).to(lo.DT[dtype])
+    w, b = ((k + 0.3 * torch.randn((C,), generator=g)).cuda() for k in (1, 0))
+    return x, w, b, repeated(g, N, S, C, dtype="fp32" if dtype == "fp32" else "bf16")
+
+
+def norm_parity(x, w, b, dout, G, act, dtype, steps, sums, part=slice(None), around=(), far=3):
+    """Forward and gradient against the float64 definition on the device, on the channels `part` (whole
+    groups).  sums: the depth of the gradient's, dweight's and dbias' sums included.  around: the
+    (length, R) of the split form's stretches.
+
+    xhat is off by steps u (m + |xhat| (1/2 + r)) for m and r the mean and rms size over the std (the mean;
+    1/std through the squares and the means of parts), layer_oracle's gradient by its sums u (m + |xhat|):
+    three times the steps cover it where r is some 1, 1 + |xhat| times the steps (`far`) where m = r is large."""
+    N, S, C = x.shape
+    with gb.GroupNorm(C, G, dtype, act=act, max_N=N) as n:
+        out, stats = n.forward(x, w, b)
+        bare, _ = n.forward(x, w, b, return_stats=False)
+        dx, dw, db = n.backward(x, w, b, stats, dout)
+    assert torch.equal(out, bare)
+    c = torch.arange(C)[part]
+    g0, g1 = int(c[0]) // (C // G), int(c[-1]) // (C // G) + 1
+    args = (x[..., part], w[part], b[part], g1 - g0, act)
+    around = torch.stack([bounds.around_pivots(x[..., part], g1 - g0, *k) for k in around]).amax(0) if around else 0.0
+    o, ob, st, sb = bounds.group_norm(*args, steps, around=around)
+    check("out", out[..., part], o, ob)
+    check("stats", stats[:, g0:g1], st, sb)
+    del o, ob
+    extra = 34 * float(torch.as_tensor(around).max())
+    ref = lo.group_norm_grad(*args, dout[..., part], sums=far * sums + extra)
+    for name, y in (("dx", dx[..., part]), ("dweight", dw[part]), ("dbias", db[part])):
+        check(name, y, *ref[name])
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp8"])
+@pytest.mark.parametrize("C,G,act", [(4096, 32, "silu"), (480, 20, "none"), (64, 8, "silu")])
+def test_rows_form_over_several_rounds(dtype, C, G, act):
+    """Blocks of 24 waves a CU forward (16 for the gradient) take four rows a thread (two) in a round:
+    two rounds and a ragged third (six and more); 16, 3 of 4 and one lane a group."""
+    P = C // G // 8
+    L = 1
+    while L < P:
+        L *= 2
+    threads = max(256, -(-G * L // 64) * 64)
+    R = threads // (G * L)
+    blocks = 16 * cus() * 64 // threads
+    N = 2 * 4 * (blocks * 3 // 2) * R + 77
+    x, w, b, dout = norm_inputs(82, N, 1, C, dtype)
+    # dweight: the rows of a thread, of a block, of 32 threads over the blocks, and a tree
+    norm_parity(x, w, b, dout, G, act, dtype, bounds.ROWS, -(-N // (blocks * R)) + R + blocks // 32 + 5 + bounds.ROWS)
