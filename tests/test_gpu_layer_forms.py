@@ -131,3 +131,45 @@ def test_rows_form_over_several_rounds(dtype, C, G, act):
     x, w, b, dout = norm_inputs(82, N, 1, C, dtype)
     # dweight: the rows of a thread, of a block, of 32 threads over the blocks, and a tree
     norm_parity(x, w, b, dout, G, act, dtype, bounds.ROWS, -(-N // (blocks * R)) + R + blocks // 32 + 5 + bounds.ROWS)
+
+
+@pytest.mark.parametrize("dtype,N,S,C,G", [("bf16", 1030, 1100, 32, 4), ("fp32", 1030, 40, 1024, 64), ("fp8", 1030, 40, 1024, 64),
+                                           ("bf16", 2100, 40, 1000, 100)])
+def test_split_form_over_rounds_of_samples(dtype, N, S, C, G):
+    """The split form takes 1,024 samples at a time and adds dweight and dbias up over such rounds.
+    Samples too large for one block (more than four rows of each of 1,024 threads), more of them than
+    CUs."""
+    V = C // 8
+    assert N > 1024 > cus() and S > 4 * (1024 // V)
+    x, w, b, dout = norm_inputs(83, N, S, C, dtype)
+    R = max(256, -(-V // 64) * 64) // V
+    n = -(-S // R)
+    # whole samples a stretch in the first rounds; down to four rows a thread in the last, of few samples
+    lengths = [rows * 4 * R for rows in range(1, -(-S // (4 * R)) + 1)]
+    steps = bounds.split(C // G, n, len(lengths))
+    norm_parity(x, w, b, dout, G, "silu", dtype, steps, steps + R + 1024 // 32 + 8, around=[(k, R) for k in lengths])
+
+
+@pytest.mark.parametrize("dtype,offset,outlier,C,G,n", [
+    ("fp32", 0.5, None, 2048, 16, 72), ("fp32", 1000.0, None, 2048, 16, 72), ("fp32", 0.5, 3e4, 2048, 16, 72),
+    ("bf16", 0.5, None, 2048, 16, 72), ("fp32", 0.5, None, 96, 16, 36), ("bf16", 3.0, None, 96, 16, 36)])
+def test_split_form_of_many_rows_a_thread(dtype, offset, outlier, C, G, n):
+    """More than 32 rows of a thread, which it sums up around a pivot each and joins, four in flight; the
+    last stretch a single row (C = 2048), and threads without a row in it (C = 96)."""
+    V = C // 8
+    R = max(256, -(-V // 64) * 64) // V
+    stretches = 16 * cus() * 64 // 256  # wanted
+    S = (stretches - 24) * n * R + 1
+    length = -(-S // (stretches * 4 * R)) * 4 * R  # whole rounds of four rows
+    assert length == n * R and n > 32
+    x, w, b, dout = norm_inputs(84, 1, S, C, dtype, 0.0 if offset > 100 else offset)
+    if offset > 100:
+        x += offset
+    if outlier:
+        x[0, 5, 0] = outlier
+    count = -(-S // length)
+    steps = bounds.split(C // G, n, count)
+    D = C // G
+    for part in (slice(0, D), slice(C - D, C)):
+        norm_parity(x, w, b, dout, G, "silu", dtype, steps, steps + n + R + count // 32 + 5, part, [(length, R)],
+                    far=8 if offset > 100 else 3)  # values up to 5 std
