@@ -257,9 +257,9 @@ int gdn_forward_noalloc(const gdn_config *cfg, const void *q, const void *k,
  * where pair i is elements (2i, 2i + 1) of the section, or (i, i +
  * axis_dim[s] / 2) with GDN_ROTARY_HALVES.  GDN_ROTARY_INVERSE turns by the
  * negative angles: the inverse, and the gradient with respect to x.  Angles are
- * formed and reduced in 64 bits (off by up to 2^-50 of their size: below 2^-24,
- * half a step of fp32 at 1, for positions up to 2^26); the turn is fp32, rounded
- * once.
+ * formed and reduced in 64 bits: off by at most 2^-50 of a radian per unit of
+ * position (2^-24, half a step of fp32 at 1, at 2^26; 2^-19 at 2^31).  The turn is
+ * fp32, rounded once.
  *
  * The turn keeps a pair's length, so q and k may be turned before the L2
  * normalisation of gdn_forward_packed: turn the first 2 H heads of the packed
