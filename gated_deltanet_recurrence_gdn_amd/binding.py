@@ -431,6 +431,7 @@ def rotary(x, axis_dims, theta=10000.0, positions=None, grid=None, first_token=0
     is read where positions are given).
     halves: pairs (i, i + dim/2) instead of (2i, 2i+1).  inverse: the negative angles, which is the
     gradient with respect to x.  out may be x (in place).  Returns out (fp32 for fp32 x, else bf16).
+    Not an autograd function: out carries no gradient, also where x requires one.
     """
     import torch
     if len(axis_dims) != 3:
@@ -523,7 +524,9 @@ class _Handle:
 class GLR(_Handle):
     """The diagonal gated linear recurrence h_t = a_t h_{t-1} + b_t v_t, for torch callers: a handle bound
     to one (device, B, H, d, dtype, gate, max_T).  gate "head": beta and decay [B, T, H]; "channel":
-    [B, T, H, d].  reverse walks the tokens from the last to the first."""
+    [B, T, H, d].  reverse walks the tokens from the last to the first.  Not an autograd function: call
+    ``backward``.  Calls on one handle must not overlap on the device (two streams, two graphs): they can
+    hang it."""
 
     def __init__(self, B, H, d, dtype="bf16", max_T=0, device=0, gate="head", reverse=False):
         self.B, self.H, self.d, self.dtype, self.device = B, H, d, dtype, device
@@ -591,7 +594,8 @@ class GLR(_Handle):
 class GroupNorm(_Handle):
     """Group norm with an activation ("silu" or "none"), channels last, for torch callers: a handle bound
     to one (device, C, G, dtype, act, eps) and samples up to max_N.  x is [N, ..., C]: every dimension
-    between is part of the sample; [N, C] normalises each row (N = B T tokens, a group per head)."""
+    between is part of the sample; [N, C] normalises each row (N = B T tokens, a group per head).  Not an
+    autograd function: call ``backward``."""
 
     def __init__(self, C, G, dtype="bf16", act="silu", eps=1e-5, max_N=1, device=0):
         self.C, self.G, self.dtype, self.device = C, G, dtype, device

@@ -263,7 +263,8 @@ int gdn_forward_noalloc(const gdn_config *cfg, const void *q, const void *k,
  *
  * The turn keeps a pair's length, so q and k may be turned before the L2
  * normalisation of gdn_forward_packed: turn the first 2 H heads of the packed
- * rows (H here = 2 * heads) in place, then call it.
+ * rows (H here = 2 * heads) in place, then call it.  FP8 q and k come out in bf16;
+ * the recurrence takes q, k and v of one type, so v is widened beside them.
  */
 #define GDN_ROTARY_HALVES 1u
 #define GDN_ROTARY_INVERSE 2u
@@ -336,8 +337,16 @@ typedef struct {
     unsigned flags;   /* GDN_FLAG_REVERSE or 0                                       */
 } gdn_glr_config;
 
-/* As gdn_create; free with gdn_free, messages from gdn_last_error.  The handle
- * owns a workspace that its calls share (see Ownership above). */
+/*
+ * As gdn_create; free with gdn_free, messages from gdn_last_error.  The handle
+ * owns a workspace that its calls share (see Ownership above): 24 bytes per
+ * channel (H * d rounded up to a multiple of 128, for each batch element) and 64
+ * tokens of max_T, and 8 per 128 channels; none where max_T <= 64.  The blocks of
+ * a call wait for each other through it.  Calls on one handle that overlap on the
+ * device (on two streams, as two graphs replayed at once, a replay beside another
+ * call) can therefore hang the device and write out of bounds, not only spoil
+ * results: order them by one stream or by events, or give each a handle.
+ */
 int gdn_glr_create(const gdn_glr_config *cfg, gdn_handle *out_h);
 
 /*
@@ -389,7 +398,8 @@ typedef struct {
 } gdn_group_norm_config;
 
 /* As gdn_create; free with gdn_free, messages from gdn_last_error.  The handle
- * owns a workspace that its calls share (see Ownership above). */
+ * owns a workspace that its calls share (see Ownership above): up to 32 MiB, and
+ * 16 C + 8 G bytes for each of up to 1,024 samples. */
 int gdn_group_norm_create(const gdn_group_norm_config *cfg, gdn_handle *out_h);
 
 /* S at most 2^30, 4 N S C below 2^62.  stats NULL = not wanted (needed by
