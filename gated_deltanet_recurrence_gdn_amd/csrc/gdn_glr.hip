@@ -25,10 +25,8 @@
 //  * A block that waits asks for one channel's words: whole rows of words in every round would
 //    fill the fabric that the tokens come through.
 //  * Two waves look back, 64 channels each, four maps at a time.  Where a call has few slabs its
-//    time is that of the chain (all its tiles run at once): there all eight waves take 16
-//    channels each and sixteen maps at a time, up to 64 tiles back (2 x 33,563 tokens of 128
-//    channels: 39 us against 66; but 6% slower at 20 slabs, where the barrier that it needs
-//    costs more than the wait).
+//    time is mostly that of the chain: there all eight waves take 16 channels each and sixteen
+//    maps at a time, up to 64 tiles back, at the price of a barrier (see few_slabs).
 //  * The block that draws a slab's last number sets the counter to the next call's number
 //    and 0, so a call leaves the workspace ready for the next one (or for its own
 //    replay in a graph) without a clearing pass.  The call's number has 32 bits.
@@ -682,6 +680,17 @@ bool fills(const GlrArgs &a, int R) {
     return a.T >= WAVES * R && slabs_of(a.B, a.H, a.d) * ((a.T + WAVES * R - 1) / (WAVES * R)) >= 4LL * a.ncu;
 }
 
+// The look-back by all waves, up to FEW slabs.  Against the other form, bf16, beta, 128 channels a
+// slab, us (forward; gradient):
+//   33,000 tokens, gates per head:     2 slabs 35 : 60; 64 : 111   4: 41 : 64; 69 : 68
+//                                      8: 56 : 69; 95 : 78   12: 67 : 73; 113 : 96   16: 83 : 72; 141 : 120
+//   33,000 tokens, gates per channel:  2 slabs 42 : 67; 65 : 110   4: 50 : 69; 87 : 117
+//                                      8: 85 : 85; 148 : 164   12: 123 : 120; 220 : 217
+//   4,680 tokens, gates per head:      2 slabs 11 : 14; 15 : 21   8: 15 : 16; 24 : 28   20: 19 : 19; 31 : 32
+//   1,500 tokens: the gradient of 2 to 8 slabs 5 to 11% less, else within 6%
+// So it gains most at the fewest slabs and costs from 16 on; in between a threshold on slabs alone
+// is not the better choice everywhere (long gradients with gates per head, which the other form
+// takes in tiles twice as long, would want 4; long forward passes with them 12).
 bool few_slabs(const GlrArgs &a, int R) { return slabs_of(a.B, a.H, a.d) <= FEW && a.T > WAVES * R; }
 
 template <int IO, bool CH, bool BETA, int R, bool FEWS = false>

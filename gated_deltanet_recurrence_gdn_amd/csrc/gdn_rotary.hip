@@ -11,11 +11,15 @@
 //    elements of a section's first half and the W of the second half that belong to them.
 //  * other halves: whole heads are staged in LDS in 16-byte vectors; a lane forms eight
 //    neighbouring outputs and finds their partners there (2 x 11,267 tokens of 26 heads of 64,
-//    halves of 2, 4 and 3, bf16: 57 us; two-byte accesses to memory instead: 116 us).
+//    halves of 2, 4 and 3, bf16: 52 us, floor 29; two-byte accesses to memory instead: 116 us).
+//    Bound by vector instructions, 46 an element and 93% of the time: each output finds its
+//    section, its partner and its angle on its own.
 // out may be x: a pair is read and written by one lane, and heads are staged whole before any
 // of them is written.
 // Measured: 2 x 32,760 tokens of 64 heads of 128 in packed rows, bf16: 358 us, 6.0 TB/s read
-// and written (a copy of 1 GB: 5.1 TB/s); 8 tokens of 40 heads: 4.3 us, the latency of one block.
+// and written (a copy of 1 GB: 5.1 TB/s); 8 tokens of 40 heads: 4.3 us, the latency of one block;
+// 1,560 tokens of 40 heads, FP8: 7.4 us, floor 4.7 (a short call waits for the frequencies, the
+// places and the angles, a barrier behind each, before its first load of x).
 #include "gdn_elem.h"
 #include "gdn_layer.h"
 
