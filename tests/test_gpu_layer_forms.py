@@ -173,3 +173,42 @@ def test_split_form_of_many_rows_a_thread(dtype, offset, outlier, C, G, n):
     for part in (slice(0, D), slice(C - D, C)):
         norm_parity(x, w, b, dout, G, "silu", dtype, steps, steps + n + R + count // 32 + 5, part, [(length, R)],
                     far=8 if offset > 100 else 3)  # values up to 5 std
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp8"])
+def test_resident_form_of_more_samples_than_blocks(dtype):
+    """A launch has at most 2^20 blocks of samples."""
+    N, S, C, G = (1 << 20) + 77, 2, 16, 4
+    x, w, b, dout = norm_inputs(85, N, S, C, dtype)
+    blocks = 16 * cus()  # of the gradient, a wave each
+    norm_parity(x, w, b, dout, G, "silu", dtype, bounds.resident(C // G), bounds.resident(C // G) + -(-N // blocks) + blocks // 32 + 64)
+
+
+@pytest.mark.parametrize("N,C,G", [(70, 8192, 1024), (1300, 4096, 2048), (3, 8192, 8192)])
+def test_rows_of_more_groups_than_the_rows_form_takes(N, C, G):
+    x, w, b, dout = norm_inputs(86, N, 1, C, "fp32", offset=0.0)
+    steps = bounds.resident(C // G)
+    norm_parity(x, w, b, dout, G, "none", "fp32", steps, steps + 64 + N)
+
+
+# ---- the diagonal recurrence over many tiles ---------------------------------------
+
+@pytest.mark.parametrize("reverse", [False, True])
+@pytest.mark.parametrize("gate", ["head", "channel"])
+@pytest.mark.parametrize("H", [1, 11])
+def test_long_look_back(H, gate, reverse):
+    """79 tiles forward and 157 for the gradient: windows of 16 tiles (11 slabs) and of 64 (one)."""
+    B, T, d = 1, 10011, 128
+    x = lo.glr_inputs(87, B, T, H, d, gate, mean=4.0)
+    c = lo.cuda(x)
+    with gb.GLR(B, H, d, max_T=T, gate=gate, reverse=reverse) as r:
+        out, st, saved = r.forward_train(c["v"], c["beta"], c["decay"], state_in=c["state"])
+        got = r.backward(c["v"], c["beta"], c["decay"], saved, c["dout"], c["dstate"])
+    h = slice(H - 1, H)
+    y = {k: (z[:, h] if k in ("state", "dstate") else z[:, :, h]) for k, z in x.items()}
+    o, ob, s, sb = lo.glr(y["v"], y["beta"], y["decay"], y["state"], reverse)
+    lo.check("out", out[:, :, h], o, ob)
+    lo.check("state_out", st[:, h], s, sb)
+    ref = lo.glr_grad(y["v"], y["beta"], y["decay"], y["dout"], y["state"], y["dstate"], reverse)
+    for name, z in zip(("dv", "dbeta", "ddecay", "dstate_in"), got):
+        lo.check(name, z[:, h] if name == "dstate_in" else z[:, :, h], *ref[name])
