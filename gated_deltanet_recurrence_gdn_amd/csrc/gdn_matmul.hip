@@ -253,11 +253,15 @@ __global__ void __launch_bounds__(64 * WM * WN) matmul_tile_kernel(const MatmulA
         read(1, pa, pw, 3);
         multiply(0);
     };
+    // Before the barrier this wave's part of the next stage is there (all of its loads but the last, which touches
+    // lines), and its last reads of the other stage, whose products come behind the barrier, are over: behind it every
+    // wave's copies write that stage anew, and the barrier itself waits for nothing.  To the compiler it is no
+    // fence either, so one stands on both sides.  (The reads went out a step of products before: no change in time.)
     const auto arrive = [&] {
-        // this wave's part of the stage is there: all of its loads but the last, which touches lines
-        if constexpr (TOUCH) asm volatile("s_waitcnt vmcnt(1)" ::: "memory");
-        else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __builtin_amdgcn_s_barrier();  // everyone's, and the other stage's reads are done
+        if constexpr (TOUCH) asm volatile("s_waitcnt vmcnt(1) lgkmcnt(0)" ::: "memory");
+        else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
     };
 #pragma unroll
     for (int i = 0; i < TM; ++i) fa[1][i] = i32x4_t{0, 0, 0, 0};
