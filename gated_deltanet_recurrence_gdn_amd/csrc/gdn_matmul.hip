@@ -205,7 +205,12 @@ __global__ void __launch_bounds__(64 * WM * WN) matmul_tile_kernel(const MatmulA
     const uint32_t ot = wave < WAVES / 2 ? (lane < SA && m0 + ta < a.M ? (uint32_t)ta * (uint32_t)a.K : NOWHERE)
                                          : (lane < SW && n0 + tw < a.N ? (uint32_t)tw * (uint32_t)a.K : NOWHERE);
     const auto touch = [&](int k) {
-        if constexpr (TOUCH) load4_to_lds(bt, k < a.K ? ot : NOWHERE, k, sink + 256 * wave);
+        if constexpr (TOUCH) {
+            // it stays the youngest load, the one that the wait before a barrier leaves under way
+            __builtin_amdgcn_sched_barrier(0);
+            load4_to_lds(bt, k < a.K ? ot : NOWHERE, k, sink + 256 * wave);
+            __builtin_amdgcn_sched_barrier(0);
+        }
     };
     i32x16_t acc[TN][TM];
 #pragma unroll
