@@ -380,14 +380,19 @@ __global__ void __launch_bounds__(64 * lin_waves(DK, DV), lin_waves(DK, DV) / (O
         const float hi = (float)x;
         sm.G[c & 1][lane] = make_float2(hi, (float)(x - hi));
         sm.w[c & 1][lane] = __builtin_amdgcn_exp2f((float)(end - x)) * a.scale_upd;
-        // A decay per head makes every chunk's factor the same, and its rounding would be raised to the number of chunks
-        // a state lives (4,096 tokens of memory: up to 1e-6): `ahead` is the logarithm of the factors' product over that
-        // of the exact ones, and each factor takes it back.  (It is off by 2^-24 |end|, and a state lives 1 / |end| chunks.)
+        // A chunk's factor comes from its logarithm in two parts, one step off however large the logarithm.  A decay per head
+        // makes every chunk's factor the same, and that step would be raised to the number of chunks a state lives (4,096
+        // tokens of memory: up to 1e-6): `ahead` is the logarithm of the factors' product over that of the exact ones, and
+        // each factor takes it back.  Only where a chunk halves the state at most: there `ahead` is known to 2^-24, while
+        // behind a strong decay (2^-99 of one token: 2^-18) it would be handed to what came in behind that decay;
+        // and what is halved oftener does not live long enough for its steps to add up.
         const double due = c == c0 ? end : end - sm.ahead;
-        const float f = __builtin_amdgcn_exp2f((float)due);
+        const float due_hi = (float)due, due_lo = (float)(due - due_hi);
+        float f = __builtin_amdgcn_exp2f(due_hi);
+        f += f * (0.69314718f * due_lo);
         if (lane == 0) {
             sm.whole[c & 1] = f;
-            sm.ahead = due > -100.0 && due < 100.0 ? (float)(log2f(f) - due) : 0.0f;
+            sm.ahead = due >= -1.0 && due <= 1.0 ? (float)(log2f(f) - due) : 0.0f;
         }
         total += end;
     };
