@@ -43,19 +43,21 @@ __device__ __forceinline__ void store8(const MatmulArgs &a, long long m, int n, 
             make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
     }
 }
-__device__ __forceinline__ void scaled4(const MatmulArgs &a, const i32x4_t &acc, float am, int n, float (&y)[4]) {
-    const float4 s = *reinterpret_cast<const float4 *>(a.w_scale + n);
-    y[0] = (float)acc[0] * (am * s.x);
-    y[1] = (float)acc[1] * (am * s.y);
-    y[2] = (float)acc[2] * (am * s.z);
-    y[3] = (float)acc[3] * (am * s.w);
-    if (a.bias) {
-        const float4 b = *reinterpret_cast<const float4 *>(a.bias + n);
-        y[0] += b.x;
-        y[1] += b.y;
-        y[2] += b.z;
-        y[3] += b.w;
+// N sums of token m's scale with their channels' scales.  The scales' product is taken first; where it leaves the
+// normal range (below it digits are lost, and a sum of zero times infinity is NaN) the sums are scaled in 64
+// bits, whose range holds any product of the three.
+template <int N>
+__device__ __forceinline__ void scaled(const int (&acc)[N], float am, const float (&s)[N], float (&y)[N]) {
+    bool within = true;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        const float p = am * s[e];
+        within &= fabsf(p) >= 0x1p-126f && fabsf(p) < __builtin_inff();
+        y[e] = (float)acc[e] * p;
     }
+    if (within) return;
+#pragma unroll 1
+    for (int e = 0; e < N; ++e) y[e] = (float)((double)acc[e] * am * s[e]);
 }
 
 // ---- few tokens: bound by the weights, each read once for up to 64 ----------------------------------
@@ -117,8 +119,16 @@ __global__ void __launch_bounds__(64 * FEW_WAVES) matmul_few_kernel(const Matmul
     const long long m = m0 + 16 * wave + l;
     const int n = n0 + 4 * g;
     if (m < a.M && n < a.N) {
+        const float4 sw = *reinterpret_cast<const float4 *>(a.w_scale + n);
         float y[4];
-        scaled4(a, s, a.a_scale[m], n, y);
+        scaled<4>({s[0], s[1], s[2], s[3]}, a.a_scale[m], {sw.x, sw.y, sw.z, sw.w}, y);
+        if (a.bias) {
+            const float4 b = *reinterpret_cast<const float4 *>(a.bias + n);
+            y[0] += b.x;
+            y[1] += b.y;
+            y[2] += b.z;
+            y[3] += b.w;
+        }
         store4<F32>(a, m, n, y);
     }
 }
@@ -308,11 +318,14 @@ __global__ void __launch_bounds__(64 * WM * WN) matmul_tile_kernel(const MatmulA
             for (int i = 0; i < TM; ++i) {
                 const long long m = m0 + wm * (BM / WM) + 32 * i + l;
                 if (m >= a.M) continue;
+                int sum[8];
                 float y[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    y[e] = (float)acc[j][i][8 * q + e] * (am[i] * s[e]);
-                    if (a.bias) y[e] += b[e];
+                for (int e = 0; e < 8; ++e) sum[e] = acc[j][i][8 * q + e];
+                scaled(sum, am[i], s, y);
+                if (a.bias) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] += b[e];
                 }
                 store8<F32>(a, m, n, y);
             }
