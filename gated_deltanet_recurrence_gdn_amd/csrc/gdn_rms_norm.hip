@@ -35,6 +35,16 @@ __device__ __forceinline__ double wave_max(double x) {
     return x;
 }
 
+// The whole number next to 127 p / top, of the two beside `middle`; ties to the even one.  p and top have 48 bits at
+// most, so 127 p and middle top do not fit 64, and their quotient does not tell which side of the middle it is on
+// (it may be as near as 2^-55 of it).  Their difference does: both products in two parts, which cancel without a rounding.
+__device__ __forceinline__ float nearest_level(double p, double top, float middle) {
+#pragma clang fp contract(off)  // the products below are rounded ones
+    const double x = 127.0 * p, y = middle * top;
+    const double d = (x - y) + (fma(127.0, p, -x) - fma((double)middle, top, -y));
+    return d == 0.0 ? rintf(middle) : d > 0.0 ? middle + 0.5f : middle - 0.5f;
+}
+
 enum RmsOut : int { RMS_SAME = 0, RMS_EIGHT = 1 };
 
 // A row's value over all of its waves: of one wave as it is, of four through LDS.
@@ -137,7 +147,7 @@ __global__ void __launch_bounds__(64 * WAVES) rms_forward_kernel(const RmsArgs a
     } else {
         // A row's factor rstd changes its scale, not its levels: they are those of h w.  The
         // product is rounded in 32 bits; where its level is next to the middle of two, and for
-        // the largest, it is taken exactly (64 bits hold it).
+        // the largest, it is taken exactly (64 bits hold it), and the level with it.
         uint32_t big = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i)
@@ -181,7 +191,7 @@ __global__ void __launch_bounds__(64 * WAVES) rms_forward_kernel(const RmsArgs a
                         const float level = (a.weight ? h[i][e] * w[e] : h[i][e]) * inv;
                         float k = rintf(level);
                         if (fabsf(level - k) > 0.499f)  // level is off by less than 1e-4
-                            k = (float)rint((double)h[i][e] * (a.weight ? (double)w[e] : 1.0) * 127.0 / exact);
+                            k = nearest_level((double)h[i][e] * (a.weight ? (double)w[e] : 1.0), exact, floorf(level) + 0.5f);
                         q = (int)k;
                     }
                     b[e / 4] |= (uint32_t)(q & 0xff) << (8 * (e % 4));
