@@ -496,7 +496,8 @@ int gdn_linear_backward(gdn_handle h, const void *q, long long q_token_stride, l
  * Root-mean-square norm with the residual's addition, over rows of C channels:
  *     h = x + residual, rounded to the type of x, and stored as sum;
  *     out = h / sqrt(mean(h^2) + eps) * weight.
- * The norm is of the stored h.  Squares are summed in fp32.
+ * The norm is of the stored h.  Squares are summed in fp32: a row whose sum of squares is beyond
+ * its range (values of 2^64) comes out as zeros, with rstd 0.
  *     x, residual, sum, out, dout, dsum, dx    [N, C]   io_dtype (GDN_F32 or GDN_BF16)
  *     weight, dweight  [C] float32 (weight NULL = 1)
  *     rstd, scale      [N] float32
@@ -525,7 +526,8 @@ int gdn_rms_norm_forward(gdn_handle h, const void *x, const void *residual, cons
 /* The same with out in 8 bits: row r stands for scale[r] * out8[r], scale = max|y| / 127, out8
  * the nearest whole number to y / scale (ties to even; decided exactly for y / rstd = h
  * weight).  A row whose largest |h weight| is below 2^-100 becomes zeros with scale 0; one
- * that holds a value that is not finite, zeros with scale NaN. */
+ * that holds a value that is not finite, or whose sum of squares or largest |h weight| is
+ * beyond the range of fp32, zeros with scale NaN. */
 int gdn_rms_norm_forward_int8(gdn_handle h, const void *x, const void *residual, const float *weight,
                               void *sum, signed char *out8, float *scale, long long N, void *hip_stream);
 
@@ -537,9 +539,10 @@ int gdn_rms_norm_backward(gdn_handle h, const void *sum, const float *weight, co
                           const void *dout, const void *dsum, void *dx, float *dweight, long long N,
                           void *hip_stream);
 
-/* Rows of x [N, C] (GDN_F32 or GDN_BF16, C a multiple of 8 up to 8192) to 8 bits with a scale
- * each, as gdn_rms_norm_forward_int8 without residual, norm and weight: weights laid out once,
- * or activations before a product.  Takes no handle: the message of a failed call is
+/* Rows of x [N, C] (GDN_F32 or GDN_BF16, C a multiple of 8 up to 8192, N up to 2^24) to 8 bits
+ * with a scale each, as gdn_rms_norm_forward_int8 without residual, norm and weight: weights
+ * laid out once, or activations before a product (whose K may be larger: operands of more than
+ * 8192 terms are the caller's to make).  Takes no handle: the message of a failed call is
  * gdn_last_error(NULL); the first call on a device checks it: make it outside graph capture. */
 int gdn_quantize_rows(int device, const void *x, int io_dtype, signed char *out8, float *scale,
                       long long N, int C, void *hip_stream);
@@ -550,11 +553,12 @@ int gdn_quantize_rows(int device, const void *x, int io_dtype, signed char *out8
  *     a [M, K], w [N, K]   signed 8-bit, contiguous (every value, -128 too)
  *     a_scale [M], w_scale, bias [N]   float32 (bias NULL = 0)
  *     out[m * out_stride + n]          GDN_F32 or GDN_BF16
- * Sums are exact; they are rounded to fp32, scaled, and rounded to out's type.  N a multiple
- * of 8, K a multiple of 16 up to 65536; out_stride >= N (in elements) a multiple of 16 bytes, so
- * out may be columns of a wider row (what lies between rows is not written).  a, w, w_scale, bias and out 16-byte
- * aligned, a_scale 4-byte.  M = 0 writes nothing.  Takes no handle: the message of a failed call is
- * gdn_last_error(NULL); the first call on a device checks it: make it outside graph capture.
+ * Sums are exact; they are rounded to fp32, scaled, and rounded to out's type.  N a multiple of 8
+ * up to 2^24, K a multiple of 16 up to 65536, (M / 128 + 1) (N / 128 + 1) at most 2^23 (quotients
+ * not rounded); out_stride (in elements) from N to 2^24 and a multiple of 16 bytes, so out may be
+ * columns of a wider row (what lies between rows is not written).  a, w, w_scale, bias and out
+ * 16-byte aligned, a_scale 4-byte.  M = 0 writes nothing.  Takes no handle: the message of a failed
+ * call is gdn_last_error(NULL); the first call on a device checks it: make it outside graph capture.
  */
 typedef struct {
     int device;       /* HIP device ordinal; -1 = dry run */
