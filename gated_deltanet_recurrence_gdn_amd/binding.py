@@ -884,8 +884,9 @@ class RMSNorm(_Handle):
 
 
 def quantize_rows(x, out=None, scale=None):
-    """Rows [..., C] of x (bf16 or fp32) in 8 bits with a scale each: (out int8, scale), x about out * scale
-    with scale = max|row| / 127.  For the weights of ``matmul_int8`` [N, K], or activations before it."""
+    """Rows [..., C] of x (bf16 or fp32, C a multiple of 8 up to 8192) in 8 bits with a scale each: (out int8,
+    scale), x about out * scale with scale = max|row| / 127.  For the weights of ``matmul_int8`` [N, K], or
+    activations before it."""
     import torch
     device = x.get_device()
     if x.dim() < 1 or device < 0 or x.dtype not in (torch.bfloat16, torch.float32) or not x.is_contiguous():
@@ -911,7 +912,7 @@ def _matmul_config(*values):
 
 def matmul_int8(a, a_scale, w, w_scale, bias=None, out=None, dtype="bf16"):
     """out[m, n] = (sum_k a[m, k] w[n, k]) a_scale[m] w_scale[n] + bias[n]: a [..., K] and w [N, K] int8 rows with
-    a scale each, bias [N] or None.  out [..., N] (fp32 or bf16; dtype where it is not given) may be the first
+    a scale each (K a multiple of 16 up to 65536, N of 8), bias [N] or None.  out [..., N] (fp32 or bf16; dtype where it is not given) may be the first
     columns of wider rows.  Returns out."""
     import torch
     device = a.get_device()

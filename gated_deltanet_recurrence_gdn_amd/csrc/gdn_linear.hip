@@ -306,7 +306,11 @@ __global__ void __launch_bounds__(256) linear_fill_kernel(float *p, const float 
 // two blocks on a CU 1.4 times one, and a pair in one piece its chunks and one more.  Measured in segments of 1, 2, 3,
 // 4 chunks: 512 tokens of 20 heads 26.6, 28.2, 31.4, 36.6 us, 1,024 36.0, 31.6, 34.5, 40.3 (320 blocks, 160, 120, 80),
 // 2,048 in 2, 3, 4 43.6, 37.4, 41.9; 200 of 4 heads 16.6 in 1, 21.9 in one piece; 2 x 32,760 of 32 heads in 128
-// (a block a CU) 1,010, in 64 810.
+// (a block a CU) 1,010, in 64 810.  These ratios are bf16's at d = 128, and are used for all sizes and types: of every
+// length there is for 4 to 600 heads of 8 to 64 chunks, d = 16 to 128, bf16 and fp32, the one chosen was the quickest or
+// within 10%, but for 64 heads of 16 chunks at d = 16 and 32 (4 chunks 20.1 and 21.1 us, 2 chunks 15.9 and 17.7; fp32 27.1
+// and 28.0, 21.7 and 23.5) and where fp32 at d = 128 has no room for two blocks on a CU (200 heads of 40 chunks: 20
+// chunks 776, one piece 632).
 int forward_seg_chunks(long long pairs, long long chunks, int ncu) {
     long long best = chunks, least = 10 * (10 * chunks + 10);
     for (int a_cu = 1; a_cu <= 2; ++a_cu) {
@@ -327,9 +331,13 @@ long long forward_most(long long pairs, long long chunks, int ncu) {
 }
 
 // The gradient: segments of at most MAX_SEG_CHUNKS chunks, and pairs in groups that share one
-// workspace.  A CU has one block of it at a time, so a segment is as long as fills the last round
-// of blocks best (a chunk's time is added for the start of each): 32,760 tokens of 20 heads in
-// segments of 14 chunks rather than 16 (dq 390 us against 411, dk and dv 442 against 466).
+// workspace.  At d = 128 a CU has one block of it at a time, so a segment is as long as fills the last
+// round of blocks best (a chunk's time is added for the start of each): 32,760 tokens of 20 heads in
+// segments of 14 chunks rather than 16 (dq 390 us against 411, dk and dv 442 against 466).  Smaller
+// heads leave room for more blocks (24 KB of LDS at d = 32), but are cut alike: of the lengths 1 to 16 for 4 to 600 heads
+// of 8 to 64 chunks the one chosen was the quickest or within 10%, but for 64 heads of 16 chunks at d = 16 and 32 (4
+// chunks 49 and 52 us, 2 chunks 42 and 46; fp32 at d = 16 69, 61) and 64 heads of 64 chunks in bf16 at d = 128 (8 chunks 448,
+// 16 chunks 389).
 struct GradCut {
     int seg_chunks, nseg, nslots, group;
     size_t slot_floats, dot_floats;  // of a group: slots of one direction, one dot array

@@ -353,6 +353,10 @@ hipError_t few_launch(const MatmulArgs &a, hipStream_t stream) {
 //   up to 16 tokens; up to 64 with N (16 + M) to 600,000 (against tiles: 32 x 12,288 x 4,096 18 us, 22; 64 x 2,560 x
 //   2,560 8.0, 13; past it 64 x 12,288 x 4,096 30, 23); more with N (16 + M) to 270,000 (400 x 640 x 2,560 11 us, 13; 192 x
 //   1,280 x 5,120 13, 22; past it 800 x 640 x 2,560 18, 14; 1,024 x 264 x 4,096 20, 19).
+// K does not enter, as the time of both grows with it: at ten sizes next to these borders and K of 256, 1,024, 2,560, 5,120 and
+// 16,384 the other side would have been quicker by up to 8%, but for 64 x 8,000 (K = 1,024: 7.6 us, tiles 9.2; 5,120: 25.3,
+// 27.8), 1,024 x 264 (1,024: 7.8, 9.2) and 100 x 2,328, whose tiles take up to 1.24 times as long (5,120: 21.9, 22.4;
+// 16,384: 63, 72).
 bool few(long long M, long long N) { return M <= 16 || N * (16 + M) <= (M <= 64 ? 600000 : 270000); }
 
 // Tiles of 256 x 256, one a CU, or of 128 x 128, two a CU, whichever rounds of blocks take less: a round of

@@ -433,7 +433,10 @@ int gdn_group_norm_backward(gdn_handle h, const void *x, const float *weight,
  * 0).  With GDN_FLAG_REVERSE the tokens are walked from T-1 to 0: state_in is then the state
  * behind the last token, state_out that of token 0.  Calls of a few tokens run as a recurrence, longer ones in
  * chunks of 64 (bf16 and FP8 inputs: products on bf16 MFMA with fp32 sums; states, and
- * gradients that leave in fp32, are held to fp32 throughout).
+ * gradients that leave in fp32, are held to fp32 throughout; for outputs that leave in bf16,
+ * scores, and for out and dv the state, are rounded to bf16 before a product, half a step each
+ * of its terms: out is about 2.3e-3 off where its own rounding is 1.7e-3.  fp32 inputs round
+ * nothing to fewer bits).
  *     q, k        io_dtype, element e of head h of token t of batch element b at
  *                 q[b * q_batch_stride + t * q_token_stride + h * d_k + e]; so they may
  *                 lie in a packed projection
